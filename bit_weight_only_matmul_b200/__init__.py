@@ -33,6 +33,9 @@ Q4_0_MAX_GROUP = 256
 Q4_0_STATIC_WS_BYTES = 64 << 20
 Q4_0_EPI_NONE, Q4_0_EPI_RESIDUAL, Q4_0_EPI_SWIGLU = 0, 1, 2
 
+Q4_TYPE_F32, Q4_TYPE_BF16, Q4_TYPE_F16, Q4_TYPE_MXFP4 = 0, 1, 2, 3
+Q4_0_MAX_NORM_DIM = 32768
+
 PATH_AUTO, PATH_GENERIC, PATH_DECODE, PATH_TENSOR, PATH_DECODE_EXACT, PATH_DECODE_TMEM, PATH_DECODE_M8 = 0, 1, 2, 3, 4, 5, 6
 
 # every symbol include/q4_0.h declares
@@ -54,11 +57,15 @@ EXPORTS = (
     "q4_0_interleave_gate_up",
     "q4_0_gather",
     "q4_0_quantize",
+    "q4_0_block_norm",
     "q4_0_selftest_wait_timeout",
     "q4_0_stream_read",
     "q4_0_device_error",
     "q4_0_force_path",
 )
+
+# every symbol include/mxfp4.h declares
+MXFP4_EXPORTS = ("mxfp4_bytes", "mxfp4_quantize", "mxfp4_dequant", "mxfp4_pack", "mxfp4_gemm")
 
 
 class Q4Error(RuntimeError):
@@ -79,6 +86,14 @@ class q4_0_problem_ex(ctypes.Structure):
     _fields_ = [("W", ctypes.c_void_p), ("X", ctypes.c_void_p), ("Y", ctypes.c_void_p),
                 ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("R", ctypes.c_void_p), ("epilogue", ctypes.c_int32)]
+
+
+class q4_0_block(ctypes.Structure):
+    _fields_ = [("y", ctypes.c_void_p), ("r", ctypes.c_void_p), ("r_out", ctypes.c_void_p), ("x", ctypes.c_void_p),
+                ("post_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+                ("M", ctypes.c_int64), ("D", ctypes.c_int64), ("gate_span", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("y_type", ctypes.c_int32), ("r_type", ctypes.c_int32), ("x_type", ctypes.c_int32)]
 
 
 def _load() -> ctypes.CDLL:
@@ -104,6 +119,12 @@ def _load() -> ctypes.CDLL:
         "q4_0_interleave_gate_up": (i32, [vp, vp, vp, i64, i64, vp]),
         "q4_0_gather": (i32, [vp, vp, vp, i64, i64, i64, vp]),
         "q4_0_quantize": (i32, [vp, vp, i64, i64, vp]),
+        "q4_0_block_norm": (i32, [ctypes.POINTER(q4_0_block), vp]),
+        "mxfp4_bytes": (i64, [i64, i64]),
+        "mxfp4_quantize": (i32, [vp, i32, vp, i64, i64, vp]),
+        "mxfp4_dequant": (i32, [vp, vp, i32, i64, i64, vp]),
+        "mxfp4_pack": (i32, [vp, vp, vp, i64, i64, vp]),
+        "mxfp4_gemm": (i32, [vp, vp, vp, i32, i64, i64, i64, vp]),
         "q4_0_device_error": (i32, [ctypes.POINTER(ctypes.c_uint32), i32]),
         "q4_0_selftest_wait_timeout": (i32, [ctypes.c_uint32, vp]),
         "q4_0_stream_read": (i32, [vp, i64, i64, vp, vp]),
@@ -259,6 +280,98 @@ def q4_0_gather(W, ids, out, T: int, V: int, D: int, stream=None) -> None:
 def q4_0_quantize(X, W, N: int, K: int, stream=None) -> None:
     """float32 X [N, K] -> Q4_0 bytes W (GGUF Q4_0 rule, bit-exact)."""
     _check(_lib.q4_0_quantize(_ptr(X), _ptr(W), N, K, _stream(stream)), "q4_0_quantize")
+
+
+_types: dict = {}
+
+
+def _type(t) -> int:
+    """The Q4_TYPE_* of a tensor's dtype, -1 for none."""
+    if not _types:
+        import torch
+        _types.update({torch.float32: Q4_TYPE_F32, torch.bfloat16: Q4_TYPE_BF16, torch.float16: Q4_TYPE_F16,
+                       torch.uint8: Q4_TYPE_MXFP4})
+    return _types.get(t.dtype, -1)
+
+
+def _operand(t, what: str, types: Sequence[int], count: int) -> int:
+    """Device address of a tensor that must be contiguous, on the current
+    device, of one of `types` and hold at least `count` elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    import torch
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what}: on device {t.get_device()}, the current device is {torch.cuda.current_device()}")
+    if _type(t) not in types:
+        raise ValueError(f"{what}: dtype {t.dtype} is not supported here")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    if t.numel() < count:
+        raise ValueError(f"{what}: {t.numel()} elements, {count} are needed")
+    return t.data_ptr()
+
+
+_VALUES = (Q4_TYPE_F32, Q4_TYPE_BF16, Q4_TYPE_F16)
+_F32, _F32_BF16, _BYTES = (Q4_TYPE_F32,), (Q4_TYPE_F32, Q4_TYPE_BF16), (Q4_TYPE_MXFP4,)
+
+
+def mxfp4_bytes(R: int, K: int) -> int:
+    """Bytes of an MXFP4 matrix of R rows by K values (include/mxfp4.h), -1
+    for sizes it cannot have."""
+    return int(_lib.mxfp4_bytes(R, K))
+
+
+def mxfp4_quantize(X, W, R: int, K: int, stream=None) -> None:
+    """X [R, K] (float32, bfloat16 or float16) to the MXFP4 matrix W (uint8,
+    mxfp4_bytes(R, K))."""
+    _check(_lib.mxfp4_quantize(_operand(X, "X", _VALUES, R * K), _type(X), _operand(W, "W", _BYTES, mxfp4_bytes(R, K)),
+                               R, K, _stream(stream)), "mxfp4_quantize")
+
+
+def mxfp4_dequant(W, out, R: int, K: int, stream=None) -> None:
+    """The values of the MXFP4 matrix W: out [R, K] float32, bfloat16 (both
+    exact) or float16."""
+    _check(_lib.mxfp4_dequant(_operand(W, "W", _BYTES, mxfp4_bytes(R, K)), _operand(out, "out", _VALUES, R * K),
+                              _type(out), R, K, _stream(stream)), "mxfp4_dequant")
+
+
+def mxfp4_pack(codes, scales, W, R: int, K: int, stream=None) -> None:
+    """codes uint8 [R, K/2] (two to a byte, the lower k in the low bits) and
+    scales uint8 [R, K/32] (E + 127) -> the MXFP4 matrix W."""
+    _check(_lib.mxfp4_pack(_operand(codes, "codes", _BYTES, R * (K // 2)), _operand(scales, "scales", _BYTES, R * (K // 32)),
+                           _operand(W, "W", _BYTES, mxfp4_bytes(R, K)), R, K, _stream(stream)), "mxfp4_pack")
+
+
+def mxfp4_gemm(W, X, Y, M: int, N: int, K: int, stream=None) -> None:
+    """Y[M,N] = X[M,K] * W[N,K]^T, W and X MXFP4 matrices (uint8), Y float32
+    or bfloat16."""
+    _check(_lib.mxfp4_gemm(_operand(W, "W", _BYTES, mxfp4_bytes(N, K)), _operand(X, "X", _BYTES, mxfp4_bytes(M, K)),
+                           _operand(Y, "Y", _F32_BF16, M * N), _type(Y), M, N, K, _stream(stream)), "mxfp4_gemm")
+
+
+def q4_0_block_norm(r, M: int, D: int, y=None, post_weight=None, gate=None, gate_span: int = 0, scale: float = 1.0,
+                    pre_weight=None, x=None, r_out=None, eps: float = 1e-6, stream=None) -> None:
+    """The norm / gate / residual step between two products on M rows of D:
+    r_out = r + scale * gate * norm(y, post_weight) and x = norm(r_out,
+    pre_weight), x float32, bfloat16 or an MXFP4 matrix (uint8).  See
+    include/q4_0.h for what may be left out."""
+    b = q4_0_block(M=M, D=D, gate_span=gate_span, scale=scale, eps=eps)
+    n = M * D
+    b.r, b.r_type = _operand(r, "r", _F32_BF16, n), _type(r)
+    if y is not None:
+        b.y, b.y_type = _operand(y, "y", _F32_BF16, n), _type(y)
+    if r_out is not None:
+        b.r_out = _operand(r_out, "r_out", (b.r_type,), n)
+    if x is not None:
+        b.x_type = _type(x)
+        b.x = _operand(x, "x", _F32_BF16 + _BYTES, mxfp4_bytes(M, D) if b.x_type == Q4_TYPE_MXFP4 else n)
+    if post_weight is not None:
+        b.post_weight = _operand(post_weight, "post_weight", _F32, D)
+    if gate is not None:
+        b.gate = _operand(gate, "gate", _F32, D * (-(-M // gate_span) if gate_span > 0 else 1))
+    if pre_weight is not None:
+        b.pre_weight = _operand(pre_weight, "pre_weight", _F32, D)
+    _check(_lib.q4_0_block_norm(ctypes.byref(b), _stream(stream)), "q4_0_block_norm")
 
 
 def q4_0_device_error(clear: bool = True) -> int:

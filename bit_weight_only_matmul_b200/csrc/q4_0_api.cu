@@ -157,6 +157,13 @@ int run_problems(const q4_0_problem *probs, int count, cudaStream_t s, void *ws 
 
 }  // namespace
 
+namespace q4 {
+
+int api_device(const DeviceInfo **out) { return current_device(out); }
+int api_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+
+}  // namespace q4
+
 extern "C" {
 
 const char *q4_0_status_string(int status) {

@@ -122,6 +122,22 @@ cudaError_t launch_prepare_x(const uint16_t *X, int64_t M, int64_t K, void *xh, 
                              cudaStream_t s);
 cudaError_t launch_prefill_prepared(const Problem &p, const void *xh, const DeviceInfo &dev, cudaStream_t s);
 
+// What the entry points of every translation unit share: the current
+// device's facts (a status code), and the record of a failed CUDA call.
+int api_device(const DeviceInfo **out);
+int api_cuda_fail(cudaError_t e);
+
+// MXFP4 (the layout: mxfp4_layout.cuh); types are Q4_TYPE_*.
+cudaError_t launch_mx_quantize(const void *X, int type, uint8_t *W, int64_t R, int64_t K, const DeviceInfo &dev,
+                               cudaStream_t s);
+cudaError_t launch_mx_dequant(const uint8_t *W, void *out, int type, int64_t R, int64_t K, const DeviceInfo &dev,
+                              cudaStream_t s);
+cudaError_t launch_mx_pack(const uint8_t *codes, const uint8_t *scales, uint8_t *W, int64_t R, int64_t K,
+                           const DeviceInfo &dev, cudaStream_t s);
+cudaError_t launch_mx_gemm(const uint8_t *W, const uint8_t *X, void *Y, int y_type, int64_t M, int64_t N, int64_t K,
+                           const DeviceInfo &dev, cudaStream_t s);
+cudaError_t launch_block_norm(const q4_0_block &b, const DeviceInfo &dev, cudaStream_t s);
+
 }  // namespace q4
 
 // ---------------------------------------------------------------------------

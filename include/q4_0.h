@@ -265,6 +265,55 @@ Q4_0_API int q4_0_gemm_grouped_ex(const q4_0_problem_ex *problems, int count, q4
 Q4_0_API int q4_0_interleave_gate_up(const void *W_gate, const void *W_up, void *W_gu,
                                      int64_t F, int64_t K, q4_0_stream_t stream);
 
+/* Element types of the operators that take more than one. */
+enum {
+    Q4_TYPE_F32 = 0,
+    Q4_TYPE_BF16 = 1,
+    Q4_TYPE_F16 = 2,
+    Q4_TYPE_MXFP4 = 3              /* an MXFP4 matrix in the layout of mxfp4.h */
+};
+
+/* Largest row length q4_0_block_norm accepts. */
+#define Q4_0_MAX_NORM_DIM 32768LL
+
+/* The step between two products of a decoder, on rows of D values:
+ *
+ *     h  = y / sqrt(mean(y^2) + eps) * post_weight     (h = y without post_weight)
+ *     r' = r + scale * gate * h                        (r' = r without y)
+ *     x  = r' / sqrt(mean(r'^2) + eps) * pre_weight    (no weight: factor 1)
+ *
+ * y [M,D] is the output of a block's last product, r [M,D] the residual
+ * stream, r' goes to r_out and x, the next product's input, to x.
+ *   y            fp32 or bf16 (y_type); NULL: the stream is only normed, and
+ *                post_weight and gate must be NULL too
+ *   r, r_out     fp32 or bf16, one type for both (r_type); r_out may be r
+ *                itself, or NULL where only x is wanted
+ *   post_weight  fp32 [D], or NULL: no norm of y
+ *   gate         fp32, or NULL: 1.  gate_span == 0: one row [D] for all rows;
+ *                otherwise row m takes gate row m / gate_span, of
+ *                ceil(M / gate_span) rows [D] (a gate per sequence or token)
+ *   x            fp32, bf16 (for q4_0_gemm) or MXFP4 (for mxfp4_gemm; x_type),
+ *                or NULL: no second norm, and pre_weight must be NULL too
+ *   pre_weight   fp32 [D], or NULL
+ * Arithmetic and sums are fp32; r' is rounded once to r_type, and x is taken
+ * from r' before that rounding.  A row of zeros with eps == 0 gives NaN. */
+typedef struct q4_0_block {
+    const void *y, *r;
+    void *r_out, *x;
+    const float *post_weight, *gate, *pre_weight;
+    int64_t M, D, gate_span;
+    float scale, eps;
+    int32_t y_type, r_type, x_type;
+} q4_0_block;
+
+/* Run that step.  All pointers 16-byte aligned; D % 32 == 0, D <=
+ * Q4_0_MAX_NORM_DIM; eps finite and >= 0; r and one of r_out and x are
+ * needed.  Apart from r_out == r nothing may overlap an output.  M == 0 or D
+ * == 0 does nothing.  The pages run an RMS norm in front of each block of the
+ * decoder; the norm behind a block, gate and scale are those of its
+ * flow-matching and sandwich-norm relatives. */
+Q4_0_API int q4_0_block_norm(const q4_0_block *block, q4_0_stream_t stream);
+
 /* Self-test of the failure detection (no counterpart on the pages): one
  * CTA waits on an on-chip barrier that nothing arrives on, bounded by
  * limit_us (1 .. 1000000); the wait gives up, ORs Q4_DEVERR_WAIT_TIMEOUT into
