@@ -156,7 +156,9 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without building the
+        # Stream object around it (4.1 us a call against 0.4)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -294,14 +296,23 @@ def _type(t) -> int:
     return _types.get(t.dtype, -1)
 
 
-def _operand(t, what: str, types: Sequence[int], count: int) -> int:
-    """Device address of a tensor that must be contiguous, on the current
-    device, of one of `types` and hold at least `count` elements."""
-    if not t.is_cuda:
+def _device(t, what: str) -> int:
+    """The current device, which `t` must be on."""
+    d = t.get_device()
+    if d < 0:
         raise ValueError(f"{what}: expected a CUDA tensor")
     import torch
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{what}: on device {t.get_device()}, the current device is {torch.cuda.current_device()}")
+    if d != torch.cuda.current_device():
+        raise ValueError(f"{what}: on device {d}, the current device is {torch.cuda.current_device()}")
+    return d
+
+
+def _operand(t, what: str, types: Sequence[int], count: int, device: int) -> int:
+    """Device address of a tensor that must be contiguous, on `device`, of one
+    of `types` and hold at least `count` elements."""
+    if (t.get_device() == device and _types.get(t.dtype, -1) in types and t.is_contiguous() and t.numel() >= count):
+        return t.data_ptr()
+    _device(t, what)
     if _type(t) not in types:
         raise ValueError(f"{what}: dtype {t.dtype} is not supported here")
     if not t.is_contiguous():
@@ -321,32 +332,42 @@ def mxfp4_bytes(R: int, K: int) -> int:
     return int(_lib.mxfp4_bytes(R, K))
 
 
+def _mx(t, what: str, R: int, K: int, device: int) -> int:
+    """Device address of an MXFP4 matrix (sizes it cannot have are refused by the library)."""
+    return _operand(t, what, _BYTES, (R + 127) // 128 * ((K + 255) // 256) * 17408, device)
+
+
 def mxfp4_quantize(X, W, R: int, K: int, stream=None) -> None:
     """X [R, K] (float32, bfloat16 or float16) to the MXFP4 matrix W (uint8,
     mxfp4_bytes(R, K))."""
-    _check(_lib.mxfp4_quantize(_operand(X, "X", _VALUES, R * K), _type(X), _operand(W, "W", _BYTES, mxfp4_bytes(R, K)),
-                               R, K, _stream(stream)), "mxfp4_quantize")
+    d = _device(X, "X")
+    _check(_lib.mxfp4_quantize(_operand(X, "X", _VALUES, R * K, d), _type(X), _mx(W, "W", R, K, d), R, K, _stream(stream)),
+           "mxfp4_quantize")
 
 
 def mxfp4_dequant(W, out, R: int, K: int, stream=None) -> None:
     """The values of the MXFP4 matrix W: out [R, K] float32, bfloat16 (both
     exact) or float16."""
-    _check(_lib.mxfp4_dequant(_operand(W, "W", _BYTES, mxfp4_bytes(R, K)), _operand(out, "out", _VALUES, R * K),
-                              _type(out), R, K, _stream(stream)), "mxfp4_dequant")
+    d = _device(W, "W")
+    _check(_lib.mxfp4_dequant(_mx(W, "W", R, K, d), _operand(out, "out", _VALUES, R * K, d), _type(out), R, K,
+                              _stream(stream)), "mxfp4_dequant")
 
 
 def mxfp4_pack(codes, scales, W, R: int, K: int, stream=None) -> None:
     """codes uint8 [R, K/2] (two to a byte, the lower k in the low bits) and
     scales uint8 [R, K/32] (E + 127) -> the MXFP4 matrix W."""
-    _check(_lib.mxfp4_pack(_operand(codes, "codes", _BYTES, R * (K // 2)), _operand(scales, "scales", _BYTES, R * (K // 32)),
-                           _operand(W, "W", _BYTES, mxfp4_bytes(R, K)), R, K, _stream(stream)), "mxfp4_pack")
+    d = _device(codes, "codes")
+    _check(_lib.mxfp4_pack(_operand(codes, "codes", _BYTES, R * (K // 2), d),
+                           _operand(scales, "scales", _BYTES, R * (K // 32), d), _mx(W, "W", R, K, d), R, K,
+                           _stream(stream)), "mxfp4_pack")
 
 
 def mxfp4_gemm(W, X, Y, M: int, N: int, K: int, stream=None) -> None:
     """Y[M,N] = X[M,K] * W[N,K]^T, W and X MXFP4 matrices (uint8), Y float32
     or bfloat16."""
-    _check(_lib.mxfp4_gemm(_operand(W, "W", _BYTES, mxfp4_bytes(N, K)), _operand(X, "X", _BYTES, mxfp4_bytes(M, K)),
-                           _operand(Y, "Y", _F32_BF16, M * N), _type(Y), M, N, K, _stream(stream)), "mxfp4_gemm")
+    d = _device(W, "W")
+    _check(_lib.mxfp4_gemm(_mx(W, "W", N, K, d), _mx(X, "X", M, K, d), _operand(Y, "Y", _F32_BF16, M * N, d), _type(Y),
+                           M, N, K, _stream(stream)), "mxfp4_gemm")
 
 
 def q4_0_block_norm(r, M: int, D: int, y=None, post_weight=None, gate=None, gate_span: int = 0, scale: float = 1.0,
@@ -355,22 +376,26 @@ def q4_0_block_norm(r, M: int, D: int, y=None, post_weight=None, gate=None, gate
     r_out = r + scale * gate * norm(y, post_weight) and x = norm(r_out,
     pre_weight), x float32, bfloat16 or an MXFP4 matrix (uint8).  See
     include/q4_0.h for what may be left out."""
-    b = q4_0_block(M=M, D=D, gate_span=gate_span, scale=scale, eps=eps)
+    d = _device(r, "r")
     n = M * D
-    b.r, b.r_type = _operand(r, "r", _F32_BF16, n), _type(r)
+    r_type = _type(r)
+    yp = op = xp = postp = gatep = prep = None
+    y_type = x_type = 0
     if y is not None:
-        b.y, b.y_type = _operand(y, "y", _F32_BF16, n), _type(y)
+        yp, y_type = _operand(y, "y", _F32_BF16, n, d), _type(y)
     if r_out is not None:
-        b.r_out = _operand(r_out, "r_out", (b.r_type,), n)
+        op = _operand(r_out, "r_out", (r_type,), n, d)
     if x is not None:
-        b.x_type = _type(x)
-        b.x = _operand(x, "x", _F32_BF16 + _BYTES, mxfp4_bytes(M, D) if b.x_type == Q4_TYPE_MXFP4 else n)
+        x_type = _type(x)
+        xp = _mx(x, "x", M, D, d) if x_type == Q4_TYPE_MXFP4 else _operand(x, "x", _F32_BF16, n, d)
     if post_weight is not None:
-        b.post_weight = _operand(post_weight, "post_weight", _F32, D)
+        postp = _operand(post_weight, "post_weight", _F32, D, d)
     if gate is not None:
-        b.gate = _operand(gate, "gate", _F32, D * (-(-M // gate_span) if gate_span > 0 else 1))
+        gatep = _operand(gate, "gate", _F32, D * (-(-M // gate_span) if gate_span > 0 else 1), d)
     if pre_weight is not None:
-        b.pre_weight = _operand(pre_weight, "pre_weight", _F32, D)
+        prep = _operand(pre_weight, "pre_weight", _F32, D, d)
+    b = q4_0_block(yp, _operand(r, "r", _F32_BF16, n, d), op, xp, postp, gatep, prep, M, D, gate_span, scale, eps, y_type,
+                   r_type, x_type)
     _check(_lib.q4_0_block_norm(ctypes.byref(b), _stream(stream)), "q4_0_block_norm")
 
 
