@@ -3,14 +3,20 @@
 //
 // Products of two E2M1 numbers and their powers of two are exact in fp32; the
 // tensor core adds them in fp32, so the sum's rounding is the only error.
-// The weight is the MMA's A operand (its 128 rows are the accumulator's
-// lanes), the activations its B operand, so that a warp's lanes hold
-// consecutive n of one row of Y and a store is one contiguous run, and a few
-// activation rows cost an MMA of few columns.
-//   * a producer thread brings the tiles of a 256-k step with bulk copies;
-//   * one thread copies the step's scales from shared to tensor memory (each
-//     ring slot has its own columns there) and issues four MMAs of K = 64;
-//   * four epilogue warps drain the accumulator and store Y.
+// The weight is the MMA's A operand (its rows are the accumulator's lanes),
+// the activations its B operand, so that a warp's lanes hold consecutive n of
+// one row of Y and a store is one contiguous run, and a few activation rows
+// cost an MMA of few columns.  Both kernels have
+//   * a producer thread that brings the tiles of a 256-k step with bulk copies;
+//   * a warp that copies the step's scales from shared to tensor memory (each
+//     ring slot has its own columns there) and issues four MMAs of K = 64.
+//     The whole warp walks the loop and one elected lane issues, so that the
+//     operands of the instructions stay in uniform registers: a step takes
+//     214 cycles at 8 activation rows and 516 at 256 (the tensor cores' full
+//     rate), where a loop under `if (lane == 0)` took 733 and 738;
+//   * epilogue warps that drain the accumulator and store Y.
+// mx_split_kernel (few rows) is paced by the weight stream from HBM,
+// mx_pair_kernel (many) by the tensor cores and the L2 that feeds them.
 #include <cstring>
 
 #include "mxfp4_layout.cuh"
@@ -21,39 +27,6 @@ namespace {
 using namespace q4dev;
 using q4::kMxCodeBytes;
 using q4::kMxTileBytes;
-
-constexpr int kThreads = 192;
-
-struct GemmParams {
-    const uint8_t *W, *X;
-    void *Y;
-    unsigned *err;
-    int64_t M, N, kt;
-    int64_t tiles_n, tiles_m;
-    int bf16;
-};
-
-// XR: activation rows a CTA's tile holds (32, 128 or 256)
-template <int XR>
-struct Cfg {
-    static constexpr int kXCodes = XR * 128;
-    static constexpr int kXTiles = (XR + 127) / 128;
-    static constexpr int kSlot = kMxTileBytes + kXCodes + 1024 * kXTiles;
-    static constexpr int kStages = XR == 32 ? 9 : XR == 128 ? 6 : 4;
-    static constexpr int kDCols = XR;
-    static constexpr int kSfCols = 8 + 8 * kXTiles;   // tensor-memory columns of a slot's scales
-    static constexpr int kTmemCols = kDCols + kStages * kSfCols <= 256 ? 256 : 512;
-    static_assert(kDCols + kStages * kSfCols <= kTmemCols, "tensor memory");
-};
-
-template <int XR>
-struct Smem {
-    uint8_t slot[Cfg<XR>::kStages][Cfg<XR>::kSlot];
-    uint64_t full[Cfg<XR>::kStages], empty[Cfg<XR>::kStages];
-    uint64_t d_full, d_empty, mma_done;
-    uint32_t tmem_base;
-    int abort_flag;
-};
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, int *abort_flag, unsigned *err) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -69,135 +42,14 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, in
     return true;
 }
 
-template <int XR>
-__global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const GemmParams P) {
-    using C = Cfg<XR>;
-    extern __shared__ uint8_t smem_raw[];
-    Smem<XR> &S = *reinterpret_cast<Smem<XR> *>(align_smem<1024>(smem_raw));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t tiles = P.tiles_n * P.tiles_m;
-    const int kt = static_cast<int>(P.kt);
+// The same answer in all lanes of a warp that waits as a whole.
+__device__ __forceinline__ bool all_lanes(bool ok) { return __all_sync(0xffffffffu, ok); }
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&S.full[s], 1);
-            mbar_init(&S.empty[s], 1);
-        }
-        mbar_init(&S.d_full, 1);
-        mbar_init(&S.d_empty, 4);
-        mbar_init(&S.mma_done, 1);
-        S.abort_flag = 0;
-        fence_mbar_init();
-    }
-    if (warp == 1) tmem_alloc(&S.tmem_base, C::kTmemCols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = S.tmem_base;
-
-    if (warp == 0) {
-        if (lane == 0) {
-            uint32_t c = 0;
-            bool ok = true;
-            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                const int64_t tn = t % P.tiles_n, m0 = t / P.tiles_n * XR;
-                // the tile's activation rows, in whole groups of eight (rows
-                // past M lie in the matrix's padding)
-                const int rows = static_cast<int>((P.M - m0 < XR ? P.M - m0 : XR) + 7) & ~7;
-                const uint8_t *w = P.W + tn * kt * kMxTileBytes;
-                const uint8_t *x = P.X + (m0 >> 7) * kt * kMxTileBytes + (m0 & 127) * 128;
-                for (int i = 0; i < kt; ++i, ++c) {
-                    const int s = c % C::kStages;
-                    if (!(ok = wait_or_abort(&S.empty[s], ((c / C::kStages) & 1) ^ 1, &S.abort_flag, P.err))) break;
-                    uint8_t *slot = S.slot[s];
-                    const int xt = (rows + 127) / 128;
-                    mbar_arrive_expect_tx(&S.full[s], kMxTileBytes + rows * 128 + 1024 * xt);
-                    bulk_g2s(slot, w + (int64_t)i * kMxTileBytes, kMxTileBytes, &S.full[s]);
-                    for (int j = 0; j < xt; ++j) {
-                        const uint8_t *xs = x + ((int64_t)j * kt + i) * kMxTileBytes;
-                        const int rj = rows - 128 * j < 128 ? rows - 128 * j : 128;
-                        bulk_g2s(slot + kMxTileBytes + j * kMxCodeBytes, xs, rj * 128, &S.full[s]);
-                        bulk_g2s(slot + kMxTileBytes + C::kXCodes + 1024 * j, xs - (m0 & 127) * 128 + kMxCodeBytes, 1024,
-                                 &S.full[s]);
-                    }
-                }
-            }
-            if (!ok)   // let the copies already issued land (bounded) before the CTA can exit
-                for (uint32_t i = 0; i < C::kStages && i < c; ++i) {
-                    const uint32_t q = c - 1 - i;
-                    mbar_wait(&S.full[q % C::kStages], (q / C::kStages) & 1, P.err);
-                }
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t c = 0, dc = 0;
-            bool ok = true;
-            for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++dc) {
-                const int64_t m0 = t / P.tiles_n * XR;
-                const int rows = static_cast<int>((P.M - m0 < XR ? P.M - m0 : XR) + 7) & ~7;
-                if (!(ok = wait_or_abort(&S.d_empty, (dc & 1) ^ 1, &S.abort_flag, P.err))) break;
-                tc_fence_after();
-                const uint32_t idesc = mxf4_idesc(128, rows, 0);
-                for (int i = 0; i < kt; ++i, ++c) {
-                    const int s = c % C::kStages;
-                    if (!(ok = wait_or_abort(&S.full[s], (c / C::kStages) & 1, &S.abort_flag, P.err))) break;
-                    tc_fence_after();
-                    const uint32_t base = smem_addr(S.slot[s]);
-                    const uint32_t sfa = tmem + C::kDCols + s * C::kSfCols, sfb = sfa + 8;
-                    #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        tc_cp_scales(sfa + 4 * g, scales_desc(base + kMxCodeBytes + 512 * g));
-                        #pragma unroll
-                        for (int j = 0; j < C::kXTiles; ++j)
-                            if (j == 0 || rows > 128)
-                                tc_cp_scales(sfb + 4 * C::kXTiles * g + 4 * j,
-                                             scales_desc(base + kMxTileBytes + C::kXCodes + 1024 * j + 512 * g));
-                    }
-                    const uint64_t a = sw128_kmajor_desc(base), b = sw128_kmajor_desc(base + kMxTileBytes);
-                    #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        tc_mma_mxf4(tmem, a + 2 * j, b + 2 * j, idesc | ((j & 1) ? mxf4_idesc(0, 0, 2) : 0u),
-                                    sfa + 4 * (j >> 1), sfb + 4 * C::kXTiles * (j >> 1), (i | j) != 0);
-                    tc_commit(&S.empty[s]);
-                }
-                if (ok) tc_commit(&S.d_full);
-            }
-            tc_commit(&S.mma_done);   // every MMA issued so far has completed once this arrives
-            wait_or_abort(&S.mma_done, 0, &S.abort_flag, P.err) || mbar_wait(&S.mma_done, 0, P.err);
-        }
-    } else {
-        const int quad = warp & 3;
-        uint32_t dc = 0;
-        for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++dc) {
-            const int64_t m0 = t / P.tiles_n * XR, n = t % P.tiles_n * 128 + 32 * quad + lane;
-            const int rows = static_cast<int>(P.M - m0 < XR ? P.M - m0 : XR);
-            if (!wait_or_abort(&S.d_full, dc & 1, &S.abort_flag, P.err)) break;
-            tc_fence_after();
-            #pragma unroll 1
-            for (int c = 0; c < rows; c += 32) {
-                float v[32];
-                tc_ld_32(tmem + (uint32_t(32 * quad) << 16) + c, v);
-                if (n < P.N) {
-                    #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (c + j < rows) {
-                            const int64_t at = (m0 + c + j) * P.N + n;
-                            if (P.bf16) static_cast<__nv_bfloat16 *>(P.Y)[at] = __float2bfloat16_rn(v[j]);
-                            else __stcs(static_cast<float *>(P.Y) + at, v[j]);
-                        }
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.d_empty);
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, C::kTmemCols);
-    }
+// One lane of a converged warp, in a form the compiler knows to be a single one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
 }
 
 // ---------------------------------------------------------------- few rows
@@ -218,6 +70,7 @@ struct SplitParams {
     int bf16;
 };
 
+constexpr int kThreads = 192;
 constexpr int kMaxSlots = 12;
 constexpr int kSplitTmemCols = 256;
 
@@ -272,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
     extern __shared__ uint8_t smem_raw[];
     __shared__ SplitSmem S;
     uint8_t *const ring = align_smem<1024>(smem_raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int slot_bytes = split_slot_bytes(P.xcap), x_bytes = split_x_bytes(P.xcap);
     float *const red = reinterpret_cast<float *>(ring + P.slots * slot_bytes);
     const int rank = static_cast<int>(blockIdx.x) % P.split;      // clusters are consecutive blocks
@@ -284,7 +137,6 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
     const int k0 = static_cast<int>(static_cast<int64_t>(P.kt) * rank / P.split);
     const int k1 = static_cast<int>(static_cast<int64_t>(P.kt) * (rank + 1) / P.split);
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int s = 0; s < P.slots; ++s) {
             mbar_init(&S.full[s], 1);
@@ -306,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
     if (P.split > 1)   // every CTA's barrier exists before another CTA arrives on it
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = S.tmem_base;
 
     if (warp == 0) {
@@ -329,32 +182,38 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
                     mbar_wait(&S.full[(c - 1 - i) % P.slots], ((c - 1 - i) / P.slots) & 1, P.err);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            bool ok = true;
-            const uint32_t idesc = mxf4_idesc(128, rows, 0);
-            const uint32_t sf0 = tmem + split_d_cols(P.xcap);
-            for (int c = 0; c < k1 - k0; ++c) {
-                const int s = c % P.slots;
-                if (!(ok = wait_or_abort(&S.full[s], (c / P.slots) & 1, &S.abort_flag, P.err))) break;
-                tc_fence_after();
-                const uint32_t base = smem_addr(ring + s * slot_bytes);
-                const uint32_t sfa = sf0 + 16 * s, sfb = sfa + 8;
+        const uint32_t idesc = mxf4_idesc(128, rows, 0);
+        const uint32_t sf0 = tmem + split_d_cols(P.xcap);
+        int s = 0;
+        uint32_t parity = 0;
+        for (int c = 0; c < k1 - k0; ++c) {
+            if (!all_lanes(wait_or_abort(&S.full[s], parity, &S.abort_flag, P.err))) break;
+            tc_fence_after();
+            const uint32_t base = smem_addr(ring) + s * slot_bytes;
+            const uint32_t sfa = sf0 + 16 * s, sfb = sfa + 8;
+            const uint64_t a = sw128_kmajor_desc(base), b = sw128_kmajor_desc(base + kMxTileBytes);
+            const uint64_t da = scales_desc(base + kMxCodeBytes), db = scales_desc(base + kMxTileBytes + x_bytes);
+            __syncwarp();
+            if (elect_one()) {
                 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    tc_cp_scales(sfa + 4 * g, scales_desc(base + kMxCodeBytes + 512 * g));
-                    tc_cp_scales(sfb + 4 * g, scales_desc(base + kMxTileBytes + x_bytes + 512 * g));
+                for (int g = 0; g < 2; ++g) {   // 512 bytes on: 32 in the descriptor's units
+                    tc_cp_scales(sfa + 4 * g, da + 32 * g);
+                    tc_cp_scales(sfb + 4 * g, db + 32 * g);
                 }
-                const uint64_t a = sw128_kmajor_desc(base), b = sw128_kmajor_desc(base + kMxTileBytes);
                 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     tc_mma_mxf4(tmem, a + 2 * j, b + 2 * j, idesc | ((j & 1) ? mxf4_idesc(0, 0, 2) : 0u),
                                 sfa + 4 * (j >> 1), sfb + 4 * (j >> 1), (c | j) != 0);
                 tc_commit(&S.empty[s]);
+                if (c == k1 - k0 - 1) tc_commit(&S.d_full);
             }
-            if (ok) tc_commit(&S.d_full);
-            tc_commit(&S.mma_done);   // every MMA issued so far has completed once this arrives
-            wait_or_abort(&S.mma_done, 0, &S.abort_flag, P.err) || mbar_wait(&S.mma_done, 0, P.err);
+            __syncwarp();
+            if (++s == P.slots) { s = 0; parity ^= 1; }
         }
+        // every MMA issued so far has completed once this commit arrives
+        if (elect_one()) tc_commit(&S.mma_done);
+        __syncwarp();
+        wait_or_abort(&S.mma_done, 0, &S.abort_flag, P.err) || mbar_wait(&S.mma_done, 0, P.err);
     } else {
         const int quad = warp & 3, row = 32 * quad + lane;
         const int64_t n = static_cast<int64_t>(tn) * 128 + row;
@@ -419,7 +278,13 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-constexpr int kSplitSmemMax = 220 * 1024, kSplitSmemHalf = 111 * 1024;
+// Shared memory of a CTA: alone on an SM, one of two, and the least it asks
+// for.  The least keeps a third CTA of this kernel, and any CTA of the other
+// tensor-memory kernels of this library (180 KB and more), off an SM that
+// holds two: their 2 x 256 columns are all there is, and a CTA that had to
+// wait for columns while the rest of its cluster holds some could wait for
+// another cluster that waits for it.
+constexpr int kSplitSmemMax = 220 * 1024, kSplitSmemHalf = 111 * 1024, kSplitSmemMin = 80 * 1024;
 
 cudaError_t launch_split(const uint8_t *W, const uint8_t *X, void *Y, bool bf16, int64_t M, int64_t N, int kt,
                          const q4::DeviceInfo &dev, cudaStream_t s) {
@@ -447,6 +312,7 @@ cudaError_t launch_split(const uint8_t *W, const uint8_t *X, void *Y, bool bf16,
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = 1024 + p.slots * split_slot_bytes(p.xcap) + split_red_bytes(p.xcap, split);
+    if (cfg.dynamicSmemBytes < kSplitSmemMin) cfg.dynamicSmemBytes = kSplitSmemMin;
     cfg.stream = s;
     cfg.attrs = attr;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -459,19 +325,236 @@ cudaError_t launch_split(const uint8_t *W, const uint8_t *X, void *Y, bool bf16,
     return cudaLaunchKernelEx(&cfg, mx_split_kernel, p);
 }
 
-template <int XR>
-cudaError_t launch(GemmParams p, const q4::DeviceInfo &dev, cudaStream_t s) {
-    constexpr size_t bytes = sizeof(Smem<XR>) + 1024;
-    static_assert(bytes <= 232448, "shared memory");
+// ---------------------------------------------------------------- many rows
+
+// The pair kernel: two CTAs of a cluster work one tile of 256 weight rows x
+// 256 activation rows as one MMA (cta_group::2): each holds 128 weight rows,
+// 128 activation rows and the accumulator of its weight rows for all 256
+// activation rows, so that a step costs a CTA 35 KB of loads instead of the
+// 52 KB of a 128 x 256 tile of its own.  Persistent, one CTA an SM.
+//   * each CTA's producer fills its own ring; in the second CTA warp 1 passes
+//     each filled slot on to the first one's barrier;
+//   * warp 1 of the first CTA issues for both and releases slots and
+//     accumulators in both with multicast commits;
+//   * eight epilogue warps take the accumulator into registers at once, so
+//     that the next tile's MMAs wait for that only, and store from there.
+struct PairParams {
+    const uint8_t *W, *X;
+    void *Y;
+    unsigned *err;
+    int64_t M, N;
+    int kt, wt, xt;           // 256-k steps, 128-row tiles of W and of X
+    int tiles_n, tiles;       // tiles of 256 x 256: along N, in all
+    int bf16;
+};
+
+constexpr int kPairThreads = 320;
+constexpr int kPairSlots = 6;
+constexpr int kPairSlotBytes = kMxTileBytes + kMxCodeBytes + 2048;   // W tile, X codes, X scales of both halves
+constexpr int kPairSfCols = 24;                                      // per slot: 8 for W, 16 for X
+static_assert(256 + kPairSlots * kPairSfCols <= 512, "tensor memory");
+
+struct PairSmem {
+    uint64_t full[kPairSlots], empty[kPairSlots];
+    uint64_t d_full, d_empty, mma_done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint64_t *bar, uint32_t rank) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_addr(smem_addr(bar), rank))
+                 : "memory");
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_pair_kernel(const __grid_constant__ PairParams P) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ PairSmem S;
+    uint8_t *const ring = align_smem<1024>(smem_raw);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(blockIdx.x) & 1;
+    const int first = static_cast<int>(blockIdx.x) >> 1, step = static_cast<int>(gridDim.x) >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairSlots; ++s) {
+            mbar_init(&S.full[s], rank == 0 ? 2 : 1);   // its own producer, and the other CTA's word
+            mbar_init(&S.empty[s], 1);
+        }
+        mbar_init(&S.d_full, 1);
+        mbar_init(&S.d_empty, 16);                      // the epilogue warps of both CTAs
+        mbar_init(&S.mma_done, 1);
+        S.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc_pair(&S.tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();   // the other CTA's barriers exist
+    tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t tmem = S.tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            int s = 0;
+            uint32_t parity = 1, issued = 0;
+            bool ok = true;
+            for (int t = first; t < P.tiles && ok; t += step) {
+                // a tile past the last of W or X: the last one again, for
+                // rows or columns of the accumulator that are not stored
+                const int wi = min(2 * (t % P.tiles_n) + rank, P.wt - 1);
+                const int x0 = 2 * (t / P.tiles_n), x1 = min(x0 + 1, P.xt - 1);
+                const uint8_t *w = P.W + static_cast<int64_t>(wi) * P.kt * kMxTileBytes;
+                const uint8_t *xa = P.X + static_cast<int64_t>(x0) * P.kt * kMxTileBytes;
+                const uint8_t *xb = P.X + static_cast<int64_t>(x1) * P.kt * kMxTileBytes;
+                for (int i = 0; i < P.kt; ++i) {
+                    if (!(ok = wait_or_abort(&S.empty[s], parity, &S.abort_flag, P.err))) break;
+                    uint8_t *slot = ring + s * kPairSlotBytes;
+                    const int64_t at = static_cast<int64_t>(i) * kMxTileBytes;
+                    mbar_arrive_expect_tx(&S.full[s], kPairSlotBytes);
+                    bulk_g2s(slot, w + at, kMxTileBytes, &S.full[s]);
+                    bulk_g2s(slot + kMxTileBytes, (rank ? xb : xa) + at, kMxCodeBytes, &S.full[s]);
+                    bulk_g2s(slot + kMxTileBytes + kMxCodeBytes, xa + at + kMxCodeBytes, 1024, &S.full[s]);
+                    bulk_g2s(slot + kMxTileBytes + kMxCodeBytes + 1024, xb + at + kMxCodeBytes, 1024, &S.full[s]);
+                    ++issued;
+                    if (++s == kPairSlots) { s = 0; parity ^= 1; }
+                }
+            }
+            if (!ok) {   // let the copies already issued land (bounded) before the CTA can exit
+                for (uint32_t i = 0; i < kPairSlots && i < issued; ++i)
+                    mbar_wait(&S.full[(issued - 1 - i) % kPairSlots], ((issued - 1 - i) / kPairSlots) & 1, P.err, 20000000ull);
+            }
+        }
+    } else if (warp == 1 && rank == 1) {
+        int s = 0;
+        uint32_t parity = 0;
+        bool ok = true;
+        for (int t = first; t < P.tiles && ok; t += step)
+            for (int i = 0; i < P.kt; ++i) {
+                if (!(ok = all_lanes(wait_or_abort(&S.full[s], parity, &S.abort_flag, P.err)))) break;
+                if (elect_one()) arrive_remote(&S.full[s], 0);
+                __syncwarp();
+                if (++s == kPairSlots) { s = 0; parity ^= 1; }
+            }
+        // the first CTA's last commit arrives here too, before this CTA may leave
+        mbar_wait(&S.mma_done, 0, P.err);
+    } else if (warp == 1) {
+        constexpr uint32_t idesc = mxf4_idesc(256, 256, 0);
+        int s = 0;
+        uint32_t parity = 0, dpar = 1;
+        bool ok = true;
+        for (int t = first; t < P.tiles && ok; t += step, dpar ^= 1) {
+            if (!(ok = all_lanes(wait_cluster_or_abort(&S.d_empty, dpar, &S.abort_flag, P.err)))) break;
+            tc_fence_after();
+            for (int i = 0; i < P.kt; ++i) {
+                if (!(ok = all_lanes(wait_cluster_or_abort(&S.full[s], parity, &S.abort_flag, P.err)))) break;
+                tc_fence_after();
+                const uint32_t base = smem_addr(ring) + s * kPairSlotBytes;
+                const uint32_t sfa = tmem + 256 + kPairSfCols * s, sfb = sfa + 8;
+                const uint64_t a = sw128_kmajor_desc(base), b = sw128_kmajor_desc(base + kMxTileBytes);
+                const uint64_t da = scales_desc(base + kMxCodeBytes), db = scales_desc(base + kMxTileBytes + kMxCodeBytes);
+                __syncwarp();
+                if (elect_one()) {
+                    #pragma unroll
+                    for (int g = 0; g < 2; ++g) {   // 512 bytes on: 32 in the descriptor's units
+                        tc_cp_scales_pair(sfa + 4 * g, da + 32 * g);
+                        tc_cp_scales_pair(sfb + 8 * g, db + 32 * g);
+                        tc_cp_scales_pair(sfb + 8 * g + 4, db + 64 + 32 * g);
+                    }
+                    #pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        tc_mma_mxf4_pair(tmem, a + 2 * j, b + 2 * j, idesc | ((j & 1) ? mxf4_idesc(0, 0, 2) : 0u),
+                                         sfa + 4 * (j >> 1), sfb + 8 * (j >> 1), (i | j) != 0);
+                    tc_commit_pair(&S.empty[s]);
+                    if (i == P.kt - 1) tc_commit_pair(&S.d_full);
+                }
+                __syncwarp();
+                if (++s == kPairSlots) { s = 0; parity ^= 1; }
+            }
+        }
+        // every MMA issued so far has completed once this commit arrives
+        if (elect_one()) tc_commit_pair(&S.mma_done);
+        __syncwarp();
+        wait_or_abort(&S.mma_done, 0, &S.abort_flag, P.err) || mbar_wait(&S.mma_done, 0, P.err);
+    } else {
+        const int quad = warp & 3, half = (warp - 2) >> 2;   // lanes [32 quad, +32), columns [128 half, +128)
+        uint32_t parity = 0;
+        for (int t = first; t < P.tiles; t += step, parity ^= 1) {
+            if (!wait_or_abort(&S.d_full, parity, &S.abort_flag, P.err)) break;
+            tc_fence_after();
+            float v[4][32];
+            #pragma unroll
+            for (int c = 0; c < 4; ++c)
+                tc_ld_cols<32>(tmem + (uint32_t(32 * quad) << 16) + 128 * half + 32 * c, v[c]);
+            tc_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_remote(&S.d_empty, 0);
+            const int64_t n = static_cast<int64_t>(2 * (t % P.tiles_n) + rank) * 128 + 32 * quad + lane;
+            const int64_t m = static_cast<int64_t>(t / P.tiles_n) * 256 + 128 * half;
+            if (n < P.N && m < P.M) {
+                const int64_t live = P.M - m;
+                #pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    #pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (32 * c + j < live) {
+                            const int64_t at = (m + 32 * c + j) * P.N + n;
+                            if (BF16) static_cast<__nv_bfloat16 *>(P.Y)[at] = __float2bfloat16_rn(v[c][j]);
+                            else static_cast<float *>(P.Y)[at] = v[c][j];
+                        }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();   // no MMA or copy of either CTA is left
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+    cluster_sync_all();
+}
+
+template <bool BF16>
+cudaError_t launch_pair(const PairParams &p, const q4::DeviceInfo &dev, cudaStream_t s) {
+    constexpr int bytes = kPairSlots * kPairSlotBytes + 1024;
     static q4::DeviceOnce configured;
+    static q4::DeviceValue resident;
     const cudaError_t e = configured.run(dev.device, [] {
-        return cudaFuncSetAttribute(mx_gemm_kernel<XR>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+        return cudaFuncSetAttribute(mx_pair_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     });
     if (e != cudaSuccess) return e;
-    p.tiles_m = (p.M + XR - 1) / XR;
-    const int64_t tiles = p.tiles_n * p.tiles_m;
-    mx_gemm_kernel<XR><<<static_cast<int>(tiles < dev.sm_count ? tiles : dev.sm_count), kThreads, bytes, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int pairs = resident.get(dev.device, [&] {
+        cudaLaunchConfig_t c = cfg;
+        cudaLaunchAttribute cl;
+        cl.id = cudaLaunchAttributeClusterDimension;
+        cl.val.clusterDim.x = 2;
+        cl.val.clusterDim.y = cl.val.clusterDim.z = 1;
+        c.gridDim = dim3(dev.sm_count / 2 * 2);
+        c.stream = nullptr;
+        c.attrs = &cl;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<BF16>, &c) != cudaSuccess) n = 0;
+        (void)cudaGetLastError();
+        return n > 0 ? n : dev.sm_count / 2;
+    });
+    cfg.gridDim = dim3(2 * (p.tiles < pairs ? p.tiles : pairs));
+    return cudaLaunchKernelEx(&cfg, mx_pair_kernel<BF16>, p);
 }
 
 }  // namespace
@@ -480,9 +563,14 @@ namespace q4 {
 
 cudaError_t launch_mx_gemm(const uint8_t *W, const uint8_t *X, void *Y, int y_type, int64_t M, int64_t N, int64_t K,
                            const DeviceInfo &dev, cudaStream_t s) {
-    GemmParams p{W, X, Y, dev.err, M, N, mx_k_tiles(K), mx_row_tiles(N), 0, y_type == Q4_TYPE_BF16};
-    if (M <= 128) return launch_split(W, X, Y, y_type == Q4_TYPE_BF16, M, N, static_cast<int>(p.kt), dev, s);
-    return launch<256>(p, dev, s);
+    const int64_t kt = mx_k_tiles(K), wt = mx_row_tiles(N), xt = mx_row_tiles(M);
+    const bool bf16 = y_type == Q4_TYPE_BF16;
+    if (M <= 128) return launch_split(W, X, Y, bf16, M, N, static_cast<int>(kt), dev, s);
+    const int64_t tiles_n = (wt + 1) / 2, tiles = tiles_n * ((xt + 1) / 2);
+    if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+    const PairParams p{W, X, Y, dev.err, M, N, static_cast<int>(kt), static_cast<int>(wt), static_cast<int>(xt),
+                       static_cast<int>(tiles_n), static_cast<int>(tiles), bf16};
+    return bf16 ? launch_pair<true>(p, dev, s) : launch_pair<false>(p, dev, s);
 }
 
 }  // namespace q4
