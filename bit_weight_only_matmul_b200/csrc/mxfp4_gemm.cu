@@ -7,7 +7,10 @@
 // the activations its B operand, so that a warp's lanes hold consecutive n of
 // one row of Y and a store is one contiguous run, and a few activation rows
 // cost an MMA of few columns.  Both kernels have
-//   * a producer thread that brings the tiles of a 256-k step with bulk copies;
+//   * producer warps that bring the tiles of a 256-k step with bulk copies. A
+//     warp issues one copy in about 100 cycles plus one for each 77 bytes, so
+//     each of the step's larger copies has a warp of its own (one warp for all
+//     of them: 1.5 times the time of a whole prompt);
 //   * a warp that copies the step's scales from shared to tensor memory (each
 //     ring slot has its own columns there) and issues four MMAs of K = 64.
 //     The whole warp walks the loop and one elected lane issues, so that the
@@ -21,6 +24,7 @@
 
 #include "mxfp4_layout.cuh"
 #include "mxfp4_tcgen05.cuh"
+#include "q4_0_tmap.cuh"
 
 namespace {
 
@@ -28,10 +32,28 @@ using namespace q4dev;
 using q4::kMxCodeBytes;
 using q4::kMxTileBytes;
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, int *abort_flag, unsigned *err) {
-    if (mbar_try_wait(bar, parity)) return true;
+// One try at phase `parity`: the thread may be suspended while it is
+// incomplete.  CLUSTER: the phase is completed by another CTA of the cluster.
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_phase(uint64_t *bar, uint32_t parity) {
+    if (!CLUSTER) return mbar_try_wait_suspend(bar, parity);
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendHintNs)
+        : "memory");
+    return ok != 0;
+}
+
+// Bounded wait that also gives up when another role has aborted.  The global
+// timer is read only once a wait has failed often enough to be out of the
+// ordinary: reading it takes longer than a step of the product.
+template <bool CLUSTER>
+__device__ __noinline__ bool long_wait(uint64_t *bar, uint32_t parity, int *abort_flag, unsigned *err) {
     const unsigned long long t0 = global_ns();
-    while (!mbar_try_wait_suspend(bar, parity)) {
+    while (!try_phase<CLUSTER>(bar, parity)) {
         if (*reinterpret_cast<volatile int *>(abort_flag)) return false;
         if (global_ns() - t0 > kWaitLimitNs) {
             atomicOr(err, (unsigned)Q4_DEVERR_WAIT_TIMEOUT);
@@ -41,9 +63,24 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, in
     }
     return true;
 }
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, int *abort_flag, unsigned *err) {
+    if (!CLUSTER && mbar_try_wait(bar, parity)) return true;
+    #pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+        if (try_phase<CLUSTER>(bar, parity)) return true;
+    return long_wait<CLUSTER>(bar, parity, abort_flag, err);
+}
 
 // The same answer in all lanes of a warp that waits as a whole.
 __device__ __forceinline__ bool all_lanes(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+// After an abort: the copies a producer has issued land (bounded) before its
+// CTA can exit.  `count` slots of a ring of `slots` were filled.
+__device__ __forceinline__ void drain(uint64_t *full, int slots, int count, unsigned *err) {
+    for (int i = 1; i <= slots && i <= count; ++i)
+        mbar_wait(&full[(count - i) % slots], ((count - i) / slots) & 1, err, 20000000ull);
+}
 
 // One lane of a converged warp, in a form the compiler knows to be a single one.
 __device__ __forceinline__ bool elect_one() {
@@ -70,7 +107,7 @@ struct SplitParams {
     int bf16;
 };
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr int kMaxSlots = 12;
 constexpr int kSplitTmemCols = 256;
 
@@ -93,26 +130,6 @@ __device__ __forceinline__ uint32_t remote_addr(uint32_t local, uint32_t rank) {
     uint32_t ra;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(local), "r"(rank));
     return ra;
-}
-
-__device__ __forceinline__ bool wait_cluster_or_abort(uint64_t *bar, uint32_t parity, int *abort_flag, unsigned *err) {
-    const unsigned long long t0 = global_ns();
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-            " selp.u32 %0, 1, 0, p;\n}"
-            : "=r"(ok)
-            : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendHintNs)
-            : "memory");
-        if (ok) return true;
-        if (*reinterpret_cast<volatile int *>(abort_flag)) return false;
-        if (global_ns() - t0 > kWaitLimitNs) {
-            atomicOr(err, (unsigned)Q4_DEVERR_WAIT_TIMEOUT);
-            *reinterpret_cast<volatile int *>(abort_flag) = 1;
-            return false;
-        }
-    }
 }
 
 __device__ __forceinline__ void store_y(const SplitParams &P, int64_t m, int64_t n, float v) {
@@ -139,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < P.slots; ++s) {
-            mbar_init(&S.full[s], 1);
+            mbar_init(&S.full[s], 2);
             mbar_init(&S.empty[s], 1);
         }
         mbar_init(&S.d_full, 1);
@@ -162,24 +179,34 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
     const uint32_t tmem = S.tmem_base;
 
     if (warp == 0) {
+        // the weight tiles
         if (lane == 0) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
             const uint8_t *w = P.W + (static_cast<int64_t>(tn) * P.kt + k0) * kMxTileBytes;
-            const uint8_t *x = P.X + ((m0 >> 7) * P.kt + k0) * kMxTileBytes;
-            bool ok = true;
             int c = 0;
-            for (; c < k1 - k0; ++c, w += kMxTileBytes, x += kMxTileBytes) {
+            for (; c < k1 - k0; ++c, w += kMxTileBytes) {
                 const int s = c % P.slots;
-                if (!(ok = wait_or_abort(&S.empty[s], ((c / P.slots) & 1) ^ 1, &S.abort_flag, P.err))) break;
-                uint8_t *slot = ring + s * slot_bytes;
-                mbar_arrive_expect_tx(&S.full[s], kMxTileBytes + rows * 128 + 1024);
-                bulk_g2s(slot, w, kMxTileBytes, &S.full[s]);
-                bulk_g2s(slot + kMxTileBytes, x, rows * 128, &S.full[s]);
-                bulk_g2s(slot + kMxTileBytes + x_bytes, x + kMxCodeBytes, 1024, &S.full[s]);
+                if (!wait_or_abort(&S.empty[s], ((c / P.slots) & 1) ^ 1, &S.abort_flag, P.err)) break;
+                mbar_arrive_expect_tx(&S.full[s], kMxTileBytes);
+                bulk_g2s(ring + s * slot_bytes, w, kMxTileBytes, &S.full[s]);
             }
-            if (!ok)   // let the copies already issued land (bounded) before the CTA can exit
-                for (int i = 0; i < P.slots && i < c; ++i)
-                    mbar_wait(&S.full[(c - 1 - i) % P.slots], ((c - 1 - i) / P.slots) & 1, P.err);
+            if (c < k1 - k0) drain(S.full, P.slots, c, P.err);
+        }
+    } else if (warp == 6) {
+        // the activation rows and their scales
+        if (lane == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            const uint8_t *x = P.X + ((m0 >> 7) * P.kt + k0) * kMxTileBytes;
+            int c = 0;
+            for (; c < k1 - k0; ++c, x += kMxTileBytes) {
+                const int s = c % P.slots;
+                if (!wait_or_abort(&S.empty[s], ((c / P.slots) & 1) ^ 1, &S.abort_flag, P.err)) break;
+                uint8_t *slot = ring + s * slot_bytes + kMxTileBytes;
+                mbar_arrive_expect_tx(&S.full[s], rows * 128 + 1024);
+                bulk_g2s(slot, x, rows * 128, &S.full[s]);
+                bulk_g2s(slot + x_bytes, x + kMxCodeBytes, 1024, &S.full[s]);
+            }
+            if (c < k1 - k0) drain(S.full, P.slots, c, P.err);
         }
     } else if (warp == 1) {
         const uint32_t idesc = mxf4_idesc(128, rows, 0);
@@ -255,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
                     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                                      remote_addr(smem_addr(&S.red_full), lane))
                                  : "memory");
-                if (rank * cpr < live && wait_cluster_or_abort(&S.red_full, 0, &S.abort_flag, P.err) && n < P.N) {
+                if (rank * cpr < live && wait_or_abort<true>(&S.red_full, 0, &S.abort_flag, P.err) && n < P.N) {
                     #pragma unroll 1
                     for (int c = rank * cpr; c < live && c < (rank + 1) * cpr; ++c) {
                         const float *p = red + (c - rank * cpr) * 128 + row;
@@ -332,23 +359,24 @@ cudaError_t launch_split(const uint8_t *W, const uint8_t *X, void *Y, bool bf16,
 // 128 activation rows and the accumulator of its weight rows for all 256
 // activation rows, so that a step costs a CTA 35 KB of loads instead of the
 // 52 KB of a 128 x 256 tile of its own.  Persistent, one CTA an SM.
-//   * each CTA's producer fills its own ring; in the second CTA warp 1 passes
-//     each filled slot on to the first one's barrier;
+//   * each CTA's producers fill its own ring, and the copies of both CTAs
+//     complete on the first one's barrier (which only copies through a tensor
+//     map can: the matrices are mapped as rows of 1 KB).  Passing the second
+//     CTA's filled slots on by remote arrivals instead held a step to 0.6 us;
 //   * warp 1 of the first CTA issues for both and releases slots and
 //     accumulators in both with multicast commits;
 //   * eight epilogue warps take the accumulator into registers at once, so
 //     that the next tile's MMAs wait for that only, and store from there.
-struct PairParams {
-    const uint8_t *W, *X;
+struct alignas(64) PairParams {
+    CUtensorMap map_w, map_x, map_xs;   // boxes: a tile, a tile's codes, a tile's scales
     void *Y;
     unsigned *err;
     int64_t M, N;
     int kt, wt, xt;           // 256-k steps, 128-row tiles of W and of X
-    int tiles_n, tiles;       // tiles of 256 x 256: along N, in all
-    int bf16;
+    int tiles_n, tiles_m, tiles;   // tiles of 256 x 256: along N, along M, in all
 };
 
-constexpr int kPairThreads = 320;
+constexpr int kPairThreads = 384;
 constexpr int kPairSlots = 6;
 constexpr int kPairSlotBytes = kMxTileBytes + kMxCodeBytes + 2048;   // W tile, X codes, X scales of both halves
 constexpr int kPairSfCols = 24;                                      // per slot: 8 for W, 16 for X
@@ -369,6 +397,46 @@ __device__ __forceinline__ void arrive_remote(uint64_t *bar, uint32_t rank) {
                  : "memory");
 }
 
+// Tile t's place: bands of up to kBand tiles along M, within a band M fastest,
+// so that the tiles worked at one time form a near square and share their
+// weight and activation tiles in L2.
+#ifndef KBAND
+#define KBAND 8
+#endif
+constexpr int kBand = KBAND;
+struct TilePlace {
+    int n, m;
+};
+__device__ __forceinline__ TilePlace place_of(const PairParams &P, int t) {
+    const int per_band = kBand * P.tiles_n, band = t / per_band, r = t - band * per_band;
+    const int rows = min(kBand, P.tiles_m - band * kBand), n = r / rows;
+    return {n, band * kBand + r - n * rows};
+}
+
+// A producer warp's walk: `copy(place, slot, step, barrier)` for each step of
+// each tile, once the slot is free; `bytes` land in each CTA.  A tile past the
+// last of W or X is the last one again, for rows or columns that are not
+// stored.
+template <class Copy>
+__device__ __forceinline__ void produce(const PairParams &P, PairSmem &S, int first, int step, int rank, int bytes, Copy &&copy) {
+    if ((threadIdx.x & 31) != 0) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int s = 0, issued = 0;
+    uint32_t parity = 1;
+    for (int t = first; t < P.tiles; t += step) {
+        const TilePlace at = place_of(P, t);
+        for (int i = 0; i < P.kt; ++i, ++issued) {
+            if (!wait_or_abort(&S.empty[s], parity, &S.abort_flag, P.err)) {
+                if (rank == 0) drain(S.full, kPairSlots, issued, P.err);
+                return;
+            }
+            if (rank == 0) mbar_arrive_expect_tx(&S.full[s], 2 * bytes);
+            copy(at, s, i, remote_addr(smem_addr(&S.full[s]), 0));
+            if (++s == kPairSlots) { s = 0; parity ^= 1; }
+        }
+    }
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_pair_kernel(const __grid_constant__ PairParams P) {
     extern __shared__ uint8_t smem_raw[];
@@ -380,7 +448,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPairSlots; ++s) {
-            mbar_init(&S.full[s], rank == 0 ? 2 : 1);   // its own producer, and the other CTA's word
+            mbar_init(&S.full[s], 3);   // the first CTA's producers, which answer for both CTAs' bytes
             mbar_init(&S.empty[s], 1);
         }
         mbar_init(&S.d_full, 1);
@@ -398,60 +466,34 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
     const uint32_t tmem = S.tmem_base;
 
     if (warp == 0) {
-        if (lane == 0) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            int s = 0;
-            uint32_t parity = 1, issued = 0;
-            bool ok = true;
-            for (int t = first; t < P.tiles && ok; t += step) {
-                // a tile past the last of W or X: the last one again, for
-                // rows or columns of the accumulator that are not stored
-                const int wi = min(2 * (t % P.tiles_n) + rank, P.wt - 1);
-                const int x0 = 2 * (t / P.tiles_n), x1 = min(x0 + 1, P.xt - 1);
-                const uint8_t *w = P.W + static_cast<int64_t>(wi) * P.kt * kMxTileBytes;
-                const uint8_t *xa = P.X + static_cast<int64_t>(x0) * P.kt * kMxTileBytes;
-                const uint8_t *xb = P.X + static_cast<int64_t>(x1) * P.kt * kMxTileBytes;
-                for (int i = 0; i < P.kt; ++i) {
-                    if (!(ok = wait_or_abort(&S.empty[s], parity, &S.abort_flag, P.err))) break;
-                    uint8_t *slot = ring + s * kPairSlotBytes;
-                    const int64_t at = static_cast<int64_t>(i) * kMxTileBytes;
-                    mbar_arrive_expect_tx(&S.full[s], kPairSlotBytes);
-                    bulk_g2s(slot, w + at, kMxTileBytes, &S.full[s]);
-                    bulk_g2s(slot + kMxTileBytes, (rank ? xb : xa) + at, kMxCodeBytes, &S.full[s]);
-                    bulk_g2s(slot + kMxTileBytes + kMxCodeBytes, xa + at + kMxCodeBytes, 1024, &S.full[s]);
-                    bulk_g2s(slot + kMxTileBytes + kMxCodeBytes + 1024, xb + at + kMxCodeBytes, 1024, &S.full[s]);
-                    ++issued;
-                    if (++s == kPairSlots) { s = 0; parity ^= 1; }
-                }
-            }
-            if (!ok) {   // let the copies already issued land (bounded) before the CTA can exit
-                for (uint32_t i = 0; i < kPairSlots && i < issued; ++i)
-                    mbar_wait(&S.full[(issued - 1 - i) % kPairSlots], ((issued - 1 - i) / kPairSlots) & 1, P.err, 20000000ull);
-            }
-        }
+        produce(P, S, first, step, rank, kMxTileBytes, [&](const TilePlace &at, int s, int i, uint32_t bar) {
+            tma_load_pair(smem_addr(ring) + s * kPairSlotBytes, &P.map_w, 17 * (min(2 * at.n + rank, P.wt - 1) * P.kt + i), bar);
+        });
+    } else if (warp == 10) {
+        produce(P, S, first, step, rank, kMxCodeBytes, [&](const TilePlace &at, int s, int i, uint32_t bar) {
+            tma_load_pair(smem_addr(ring) + s * kPairSlotBytes + kMxTileBytes, &P.map_x,
+                          17 * (min(2 * at.m + rank, P.xt - 1) * P.kt + i), bar);
+        });
+    } else if (warp == 11) {
+        produce(P, S, first, step, rank, 2048, [&](const TilePlace &at, int s, int i, uint32_t bar) {
+            #pragma unroll
+            for (int h = 0; h < 2; ++h)
+                tma_load_pair(smem_addr(ring) + s * kPairSlotBytes + kMxTileBytes + kMxCodeBytes + 1024 * h, &P.map_xs,
+                              17 * (min(2 * at.m + h, P.xt - 1) * P.kt + i) + 16, bar);
+        });
     } else if (warp == 1 && rank == 1) {
-        int s = 0;
-        uint32_t parity = 0;
-        bool ok = true;
-        for (int t = first; t < P.tiles && ok; t += step)
-            for (int i = 0; i < P.kt; ++i) {
-                if (!(ok = all_lanes(wait_or_abort(&S.full[s], parity, &S.abort_flag, P.err)))) break;
-                if (elect_one()) arrive_remote(&S.full[s], 0);
-                __syncwarp();
-                if (++s == kPairSlots) { s = 0; parity ^= 1; }
-            }
         // the first CTA's last commit arrives here too, before this CTA may leave
-        mbar_wait(&S.mma_done, 0, P.err);
+        wait_or_abort(&S.mma_done, 0, &S.abort_flag, P.err) || mbar_wait(&S.mma_done, 0, P.err);
     } else if (warp == 1) {
         constexpr uint32_t idesc = mxf4_idesc(256, 256, 0);
         int s = 0;
         uint32_t parity = 0, dpar = 1;
         bool ok = true;
         for (int t = first; t < P.tiles && ok; t += step, dpar ^= 1) {
-            if (!(ok = all_lanes(wait_cluster_or_abort(&S.d_empty, dpar, &S.abort_flag, P.err)))) break;
+            if (!(ok = all_lanes(wait_or_abort<true>(&S.d_empty, dpar, &S.abort_flag, P.err)))) break;
             tc_fence_after();
             for (int i = 0; i < P.kt; ++i) {
-                if (!(ok = all_lanes(wait_cluster_or_abort(&S.full[s], parity, &S.abort_flag, P.err)))) break;
+                if (!(ok = all_lanes(wait_or_abort(&S.full[s], parity, &S.abort_flag, P.err)))) break;
                 tc_fence_after();
                 const uint32_t base = smem_addr(ring) + s * kPairSlotBytes;
                 const uint32_t sfa = tmem + 256 + kPairSfCols * s, sfb = sfa + 8;
@@ -494,8 +536,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_remote(&S.d_empty, 0);
-            const int64_t n = static_cast<int64_t>(2 * (t % P.tiles_n) + rank) * 128 + 32 * quad + lane;
-            const int64_t m = static_cast<int64_t>(t / P.tiles_n) * 256 + 128 * half;
+            const TilePlace at_tile = place_of(P, t);
+            const int64_t n = static_cast<int64_t>(2 * at_tile.n + rank) * 128 + 32 * quad + lane;
+            const int64_t m = static_cast<int64_t>(at_tile.m) * 256 + 128 * half;
             if (n < P.N && m < P.M) {
                 const int64_t live = P.M - m;
                 #pragma unroll
@@ -568,8 +611,21 @@ cudaError_t launch_mx_gemm(const uint8_t *W, const uint8_t *X, void *Y, int y_ty
     if (M <= 128) return launch_split(W, X, Y, bf16, M, N, static_cast<int>(kt), dev, s);
     const int64_t tiles_n = (wt + 1) / 2, tiles = tiles_n * ((xt + 1) / 2);
     if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
-    const PairParams p{W, X, Y, dev.err, M, N, static_cast<int>(kt), static_cast<int>(wt), static_cast<int>(xt),
-                       static_cast<int>(tiles_n), static_cast<int>(tiles), bf16};
+    if (17 * wt * kt > 0x7fffffff || 17 * xt * kt > 0x7fffffff) return cudaErrorInvalidValue;
+    PairParams p;
+    if (!encode_1k_rows_map(&p.map_w, W, 17 * wt * kt, 17) || !encode_1k_rows_map(&p.map_x, X, 17 * xt * kt, 16) ||
+        !encode_1k_rows_map(&p.map_xs, X, 17 * xt * kt, 1))
+        return cudaErrorInvalidValue;
+    p.Y = Y;
+    p.err = dev.err;
+    p.M = M;
+    p.N = N;
+    p.kt = static_cast<int>(kt);
+    p.wt = static_cast<int>(wt);
+    p.xt = static_cast<int>(xt);
+    p.tiles_n = static_cast<int>(tiles_n);
+    p.tiles_m = static_cast<int>((xt + 1) / 2);
+    p.tiles = static_cast<int>(tiles);
     return bf16 ? launch_pair<true>(p, dev, s) : launch_pair<false>(p, dev, s);
 }
 

@@ -84,6 +84,18 @@ namespace q4 {
 
 bool tensor_maps_available() { return encoder() != nullptr; }
 
+bool encode_1k_rows_map(CUtensorMap *out, const void *ptr, int64_t rows, int box_rows) {
+    EncodeTiled enc = encoder();
+    if (!enc) return false;
+    const cuuint32_t estr[2] = {1, 1};
+    const cuuint64_t dims[2] = {256, static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {1024};
+    const cuuint32_t box[2] = {256, static_cast<cuuint32_t>(box_rows)};
+    return enc(out, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool get_tensor_map(CUtensorMap *out, const void *ptr, int64_t rows, int64_t cols, int kind) {
     const Key k{ptr, rows, cols, kind};
     std::lock_guard<std::mutex> lock(g_mu);

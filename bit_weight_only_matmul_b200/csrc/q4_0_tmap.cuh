@@ -22,4 +22,8 @@ bool tensor_maps_available();
 // type); cached per (ptr, rows, cols, kind).  False if it cannot be encoded.
 bool get_tensor_map(CUtensorMap *out, const void *ptr, int64_t rows, int64_t cols, int kind);
 
+// The map of `ptr` viewed as `rows` rows of 256 32-bit words (1 KB), box of
+// box_rows whole rows, no swizzle; encoded anew by each call, nothing kept.
+bool encode_1k_rows_map(CUtensorMap *out, const void *ptr, int64_t rows, int box_rows);
+
 }  // namespace q4
