@@ -21,6 +21,7 @@
 // mx_split_kernel (few rows) is paced by the weight stream from HBM,
 // mx_pair_kernel (many) by the tensor cores and the L2 that feeds them.
 #include <cstring>
+#include <type_traits>
 
 #include "mxfp4_layout.cuh"
 #include "mxfp4_tcgen05.cuh"
@@ -392,10 +393,16 @@ struct PairSmem {
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Says that this warp has read its part of the accumulator.  Relaxed: what it
+// read is in registers (tcgen05.wait::ld), it hands over no memory, and a
+// release would wait for the last tile's stores of Y.
 __device__ __forceinline__ void arrive_remote(uint64_t *bar, uint32_t rank) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_addr(smem_addr(bar), rank))
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_addr(smem_addr(bar), rank))
                  : "memory");
 }
+
+__device__ __forceinline__ void put(float *y, float v) { *y = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *y, float v) { *y = __float2bfloat16_rn(v); }
 
 // Tile t's place: bands of up to kBand tiles along M, within a band M fastest,
 // so that the tiles worked at one time form a near square and share their
@@ -490,7 +497,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
         uint32_t parity = 0, dpar = 1;
         bool ok = true;
         for (int t = first; t < P.tiles && ok; t += step, dpar ^= 1) {
-            if (!(ok = all_lanes(wait_or_abort<true>(&S.d_empty, dpar, &S.abort_flag, P.err)))) break;
+            if (!(ok = all_lanes(wait_or_abort(&S.d_empty, dpar, &S.abort_flag, P.err)))) break;
             tc_fence_after();
             for (int i = 0; i < P.kt; ++i) {
                 if (!(ok = all_lanes(wait_or_abort(&S.full[s], parity, &S.abort_flag, P.err)))) break;
@@ -540,16 +547,23 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
             const int64_t n = static_cast<int64_t>(2 * at_tile.n + rank) * 128 + 32 * quad + lane;
             const int64_t m = static_cast<int64_t>(at_tile.m) * 256 + 128 * half;
             if (n < P.N && m < P.M) {
-                const int64_t live = P.M - m;
-                #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                // whole tiles without a test for each row: with one, storing a
+                // tile took longer (9600 cycles) than the MMAs of 18 steps
+                using T = typename std::conditional<BF16, __nv_bfloat16, float>::type;
+                T *y = static_cast<T *>(P.Y) + m * P.N + n;
+                const int live = static_cast<int>(P.M - m < 128 ? P.M - m : 128);
+                if (live == 128) {
                     #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (32 * c + j < live) {
-                            const int64_t at = (m + 32 * c + j) * P.N + n;
-                            if (BF16) static_cast<__nv_bfloat16 *>(P.Y)[at] = __float2bfloat16_rn(v[c][j]);
-                            else static_cast<float *>(P.Y)[at] = v[c][j];
-                        }
+                    for (int c = 0; c < 4; ++c)
+                        #pragma unroll
+                        for (int j = 0; j < 32; ++j, y += P.N) put(y, v[c][j]);
+                } else {
+                    #pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        #pragma unroll
+                        for (int j = 0; j < 32; ++j, y += P.N)
+                            if (32 * c + j < live) put(y, v[c][j]);
+                }
             }
         }
     }
