@@ -128,12 +128,9 @@ int api_device(const DeviceInfo **out);
 int api_cuda_fail(cudaError_t e);
 
 // MXFP4 (the layout: mxfp4_layout.cuh); types are Q4_TYPE_*.
-cudaError_t launch_mx_quantize(const void *X, int type, uint8_t *W, int64_t R, int64_t K, const DeviceInfo &dev,
-                               cudaStream_t s);
-cudaError_t launch_mx_dequant(const uint8_t *W, void *out, int type, int64_t R, int64_t K, const DeviceInfo &dev,
-                              cudaStream_t s);
-cudaError_t launch_mx_pack(const uint8_t *codes, const uint8_t *scales, uint8_t *W, int64_t R, int64_t K,
-                           const DeviceInfo &dev, cudaStream_t s);
+cudaError_t launch_mx_quantize(const void *X, int type, uint8_t *W, int64_t R, int64_t K, cudaStream_t s);
+cudaError_t launch_mx_dequant(const uint8_t *W, void *out, int type, int64_t R, int64_t K, cudaStream_t s);
+cudaError_t launch_mx_pack(const uint8_t *codes, const uint8_t *scales, uint8_t *W, int64_t R, int64_t K, cudaStream_t s);
 cudaError_t launch_mx_gemm(const uint8_t *W, const uint8_t *X, void *Y, int y_type, int64_t M, int64_t N, int64_t K,
                            const DeviceInfo &dev, cudaStream_t s);
 cudaError_t launch_block_norm(const q4_0_block &b, const DeviceInfo &dev, cudaStream_t s);
@@ -273,6 +270,32 @@ __device__ __forceinline__ void bulk_g2s_u32(uint32_t dst, const void *src, uint
         "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
         "l"(src), "r"(bytes), "r"(smem_addr(bar))
         : "memory");
+}
+
+// The start of a kernel launched with launch_dependent(): the next kernel's
+// CTAs may come up from now on, and nothing before this kernel on the stream
+// is still running once it returns.
+__device__ __forceinline__ void begin_dependent() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Launch with programmatic stream serialization: the CTAs come up while the
+// kernel before is ending, so the kernel must call begin_dependent() before it
+// touches global memory.
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t s, A... args) {
+    if (grid < 1 || grid > 0x7fffffff) return cudaErrorInvalidValue;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {

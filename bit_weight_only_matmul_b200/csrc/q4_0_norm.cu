@@ -33,15 +33,11 @@ __device__ __forceinline__ float block_sum(float v, float *part) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    const int warps = blockDim.x >> 5;
-    float s = 0.f;
-    for (int w = 0; w < warps; ++w) s += part[w];
+    // every warp adds the line itself: the same order, the same bits in all lanes
+    float s = (threadIdx.x & 31) < (blockDim.x >> 5) ? part[threadIdx.x & 31] : 0.f;
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
-}
-
-__device__ __forceinline__ void load8_any(const void *p, int type, int64_t at, float (&v)[8]) {
-    if (type == Q4_TYPE_F32) load8(static_cast<const float *>(p) + at, v);
-    else load8(static_cast<const __nv_bfloat16 *>(p) + at, v);
 }
 
 __device__ __forceinline__ void weights8(const float *p, float (&v)[8]) {
@@ -66,68 +62,88 @@ __device__ __forceinline__ void store8_any(void *p, int type, int64_t at, const 
     }
 }
 
-template <int G>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
+// G: groups of eight values a thread holds; T: threads at most; YT, RT: the
+// types of y and r.
+template <int G, int T, class YT, class RT>
+__global__ void __launch_bounds__(T, G == 2 && T == 512 ? 2 : 1) block_norm_kernel(const __grid_constant__ NormParams P) {
     __shared__ float part[2][32];
+    begin_dependent();
     const int lane = threadIdx.x & 31;
+    const int D = static_cast<int>(P.D), gap = 8 * blockDim.x;
     for (int64_t row = blockIdx.x; row < P.M; row += gridDim.x) {
-        float v[G][8];   // y, then r'
-        float ss = 0.f;
-        if (P.y) {
-            #pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const int64_t k = 8 * (threadIdx.x + (int64_t)j * blockDim.x);
-                if (k < P.D) {
-                    load8_any(P.y, P.y_type, row * P.D + k, v[j]);
-                    #pragma unroll
-                    for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
-                }
-            }
-        }
-        float fy = P.scale;
-        if (P.y && P.post) fy *= rsqrtf(block_sum(ss, part[0]) / static_cast<float>(P.D) + P.eps);
-        const float *gate = P.gate ? P.gate + (P.gate_span ? row / P.gate_span : 0) * P.D : nullptr;
-        ss = 0.f;
+        const int64_t at = row * P.D;
+        // both rows on their way before the first sum
+        Raw8<YT> y[G];
+        Raw8<RT> r[G];
         #pragma unroll
         for (int j = 0; j < G; ++j) {
-            const int64_t k = 8 * (threadIdx.x + (int64_t)j * blockDim.x);
-            if (k < P.D) {
-                float r[8], w[8];
-                load8_any(P.r, P.r_type, row * P.D + k, r);
+            const int k = 8 * threadIdx.x + j * gap;
+            if (k < D && P.y) y[j].load(P.y, at + k);
+        }
+        #pragma unroll
+        for (int j = 0; j < G; ++j) {
+            const int k = 8 * threadIdx.x + j * gap;
+            if (k < D) r[j].load(P.r, at + k);
+        }
+        float fy = P.scale;
+        if (P.y && P.post) {
+            float ss = 0.f;
+            #pragma unroll
+            for (int j = 0; j < G; ++j)
+                if (8 * threadIdx.x + j * gap < D) {
+                    float v[8];
+                    y[j].get(v);
+                    #pragma unroll
+                    for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+                }
+            fy *= rsqrtf(block_sum(ss, part[0]) / static_cast<float>(D) + P.eps);
+        }
+        const float *gate = P.gate ? P.gate + (P.gate_span ? row / P.gate_span : 0) * P.D : nullptr;
+        float v[G][8];   // r'
+        float ss = 0.f;
+        #pragma unroll
+        for (int j = 0; j < G; ++j) {
+            const int k = 8 * threadIdx.x + j * gap;
+            if (k < D) {
+                r[j].get(v[j]);
                 if (P.y) {
+                    float h[8], w[8];
+                    y[j].get(h);
                     if (P.post) {
                         weights8(P.post + k, w);
                         #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[j][i] *= w[i];
+                        for (int i = 0; i < 8; ++i) h[i] *= w[i];
                     }
                     if (gate) {
                         weights8(gate + k, w);
                         #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[j][i] *= w[i];
+                        for (int i = 0; i < 8; ++i) h[i] *= w[i];
                     }
                     #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[j][i] = fmaf(v[j][i], fy, r[i]);
-                } else {
-                    #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[j][i] = r[i];
+                    for (int i = 0; i < 8; ++i) v[j][i] = fmaf(h[i], fy, v[j][i]);
                 }
-                if (P.r_out) store8_any(P.r_out, P.r_type, row * P.D + k, v[j]);
+                if (P.r_out) store8_any(P.r_out, P.r_type, at + k, v[j]);
                 #pragma unroll
                 for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
             }
         }
         if (P.x) {
-            const float fx = rsqrtf(block_sum(ss, part[1]) / static_cast<float>(P.D) + P.eps);
+            const float fx = rsqrtf(block_sum(ss, part[1]) / static_cast<float>(D) + P.eps);
             #pragma unroll
             for (int j = 0; j < G; ++j) {
-                const int64_t k = 8 * (threadIdx.x + (int64_t)j * blockDim.x);
-                const bool live = k < P.D;
+                const int k = 8 * threadIdx.x + j * gap;
+                const bool live = k < D;
                 if (live) {
-                    float w[8];
-                    if (P.pre) weights8(P.pre + k, w);
-                    #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * fx * (P.pre ? w[i] : 1.0f);
-                    if (P.x_type != Q4_TYPE_MXFP4) store8_any(P.x, P.x_type, row * P.D + k, v[j]);
+                    if (P.pre) {
+                        float w[8];
+                        weights8(P.pre + k, w);
+                        #pragma unroll
+                        for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * fx * w[i];
+                    } else {
+                        #pragma unroll
+                        for (int i = 0; i < 8; ++i) v[j][i] *= fx;
+                    }
+                    if (P.x_type != Q4_TYPE_MXFP4) store8_any(P.x, P.x_type, at + k, v[j]);
                 }
                 if (P.x_type == Q4_TYPE_MXFP4 && (k >> 8) < P.kt) {   // the whole warp: k >> 8 is the warp's tile
                     if (!live) {
@@ -148,10 +164,14 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
     }
 }
 
-template <int G>
-cudaError_t launch(const NormParams &p, int threads, int grid, cudaStream_t s) {
-    block_norm_kernel<G><<<grid, threads, 0, s>>>(p);
-    return cudaGetLastError();
+template <int G, int T>
+cudaError_t launch(const NormParams &p, int threads, int64_t grid, cudaStream_t s) {
+    const bool yf = p.y_type == Q4_TYPE_F32, rf = p.r_type == Q4_TYPE_F32;
+    using B = __nv_bfloat16;
+    return yf ? rf ? launch_dependent(block_norm_kernel<G, T, float, float>, grid, threads, s, p)
+                   : launch_dependent(block_norm_kernel<G, T, float, B>, grid, threads, s, p)
+              : rf ? launch_dependent(block_norm_kernel<G, T, B, float>, grid, threads, s, p)
+                   : launch_dependent(block_norm_kernel<G, T, B, B>, grid, threads, s, p);
 }
 
 }  // namespace
@@ -173,15 +193,20 @@ cudaError_t launch_block_norm(const q4_0_block &b, const DeviceInfo &dev, cudaSt
     p.kt = mx_k_tiles(b.D);
     p.scale = b.scale;
     p.eps = b.eps;
-    p.y_type = b.y_type;
+    p.y_type = b.y ? b.y_type : Q4_TYPE_F32;
     p.r_type = b.r_type;
     p.x_type = b.x_type;
+    // few rows: as many threads as the row has groups, for the shortest time
+    // of a row; many: two or four groups a thread, so that a CTA's sums hold
+    // up fewer warps and several CTAs fit on an SM
     const int64_t groups = b.D / 8;
-    const int G = groups <= 1024 ? 1 : groups <= 2048 ? 2 : 4;
+    const bool few = b.M <= dev.sm_count;
+    const int G = groups <= (few ? 1024 : 256) ? 1 : groups <= (few ? 2048 : 1024) ? 2 : 4;
     const int threads = static_cast<int>(((groups + G - 1) / G + 31) / 32 * 32);
-    const int64_t cap = static_cast<int64_t>(dev.sm_count) * 64;
-    const int grid = static_cast<int>(b.M < cap ? b.M : cap);
-    return G == 1 ? launch<1>(p, threads, grid, s) : G == 2 ? launch<2>(p, threads, grid, s) : launch<4>(p, threads, grid, s);
+    const int64_t cap = static_cast<int64_t>(dev.sm_count) * 64, grid = b.M < cap ? b.M : cap;
+    if (G == 1) return launch<1, 1024>(p, threads, grid, s);
+    if (threads <= 512) return G == 2 ? launch<2, 512>(p, threads, grid, s) : launch<4, 512>(p, threads, grid, s);
+    return G == 2 ? launch<2, 1024>(p, threads, grid, s) : launch<4, 1024>(p, threads, grid, s);
 }
 
 }  // namespace q4
