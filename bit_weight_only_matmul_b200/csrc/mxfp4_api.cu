@@ -37,7 +37,7 @@ int mxfp4_quantize(const void *X, int x_type, void *W, int64_t R, int64_t K, q4_
     const q4::DeviceInfo *dev = nullptr;
     st = q4::api_device(&dev);
     if (st != Q4_OK) return st;
-    return done(q4::launch_mx_quantize(X, x_type, static_cast<uint8_t *>(W), R, K,
+    return done(q4::launch_mx_quantize(X, x_type, static_cast<uint8_t *>(W), R, K, *dev,
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -51,7 +51,7 @@ int mxfp4_dequant(const void *W, void *out, int out_type, int64_t R, int64_t K, 
     const q4::DeviceInfo *dev = nullptr;
     st = q4::api_device(&dev);
     if (st != Q4_OK) return st;
-    return done(q4::launch_mx_dequant(static_cast<const uint8_t *>(W), out, out_type, R, K,
+    return done(q4::launch_mx_dequant(static_cast<const uint8_t *>(W), out, out_type, R, K, *dev,
                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -92,19 +92,19 @@ __device__ __forceinline__ bool elect_one() {
 
 // ---------------------------------------------------------------- few rows
 
-// The split kernel: a cluster of `split` CTAs takes one tile of 128 weight
-// rows x up to 128 activation rows, each CTA a run of its 256-k steps.  The
-// ranks' sums meet in shared memory: rank q adds columns [q*cpr, (q+1)*cpr)
-// over all ranks, in rank order, so the result does not depend on timing.
+// The split kernel: a cluster of `split` CTAs takes 128 weight rows and all
+// activation rows (up to 32), each CTA a run of the 256-k steps.  The ranks'
+// sums meet in shared memory: rank q adds columns [q*cpr, (q+1)*cpr) over all
+// ranks, in rank order, so the result does not depend on timing.
 struct SplitParams {
     const uint8_t *W, *X;
     void *Y;
     unsigned *err;
-    int64_t M, N;
-    int kt, tiles_n;
+    int64_t N;
+    int M, kt;
     int split;        // CTAs of a cluster
     int slots;        // ring slots
-    int xcap;         // activation rows a slot has room for (a multiple of 8)
+    int xcap;         // M in whole groups of eight rows (the rest lies in X's padding)
     int bf16;
 };
 
@@ -127,13 +127,16 @@ __host__ __device__ constexpr int split_red_bytes(int xcap, int split) {
 }
 __host__ __device__ constexpr int split_d_cols(int xcap) { return (xcap + 15) & ~15; }
 
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t remote_addr(uint32_t local, uint32_t rank) {
     uint32_t ra;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(local), "r"(rank));
     return ra;
 }
 
-__device__ __forceinline__ void store_y(const SplitParams &P, int64_t m, int64_t n, float v) {
+__device__ __forceinline__ void store_y(const SplitParams &P, int m, int64_t n, float v) {
     const int64_t at = m * P.N + n;
     if (P.bf16) static_cast<__nv_bfloat16 *>(P.Y)[at] = __float2bfloat16_rn(v);
     else static_cast<float *>(P.Y)[at] = v;
@@ -147,11 +150,8 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
     const int slot_bytes = split_slot_bytes(P.xcap), x_bytes = split_x_bytes(P.xcap);
     float *const red = reinterpret_cast<float *>(ring + P.slots * slot_bytes);
     const int rank = static_cast<int>(blockIdx.x) % P.split;      // clusters are consecutive blocks
-    const int tile = static_cast<int>(blockIdx.x) / P.split;
-    const int tn = tile % P.tiles_n;
-    const int64_t m0 = static_cast<int64_t>(tile / P.tiles_n) * 128;
-    const int live = static_cast<int>(P.M - m0 < 128 ? P.M - m0 : 128);
-    const int rows = (live + 7) & ~7;
+    const int tn = static_cast<int>(blockIdx.x) / P.split;
+    const int live = P.M, rows = P.xcap;
     const int k0 = static_cast<int>(static_cast<int64_t>(P.kt) * rank / P.split);
     const int k1 = static_cast<int>(static_cast<int64_t>(P.kt) * (rank + 1) / P.split);
 
@@ -173,8 +173,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
     if (warp == 1) tmem_alloc(&S.tmem_base, kSplitTmemCols);
     tc_fence_before();
     __syncthreads();
-    if (P.split > 1)   // every CTA's barrier exists before another CTA arrives on it
-        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (P.split > 1) cluster_sync_all();   // every CTA's barrier exists before another CTA arrives on it
     tc_fence_after();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = S.tmem_base;
@@ -197,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
         // the activation rows and their scales
         if (lane == 0) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            const uint8_t *x = P.X + ((m0 >> 7) * P.kt + k0) * kMxTileBytes;
+            const uint8_t *x = P.X + static_cast<int64_t>(k0) * kMxTileBytes;
             int c = 0;
             for (; c < k1 - k0; ++c, x += kMxTileBytes) {
                 const int s = c % P.slots;
@@ -242,55 +241,54 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
         if (elect_one()) tc_commit(&S.mma_done);
         __syncwarp();
         wait_or_abort(&S.mma_done, 0, &S.abort_flag, P.err) || mbar_wait(&S.mma_done, 0, P.err);
-    } else {
-        const int quad = warp & 3, row = 32 * quad + lane;
-        const int64_t n = static_cast<int64_t>(tn) * 128 + row;
-        const uint32_t d = tmem + (uint32_t(32 * quad) << 16);
-        if (wait_or_abort(&S.d_full, 0, &S.abort_flag, P.err)) {
-            tc_fence_after();
-            if (P.split == 1) {
-                #pragma unroll 1
-                for (int c = 0; c < live; c += 8) {
-                    float v[8];
-                    tc_ld_cols<8>(d + c, v);
-                    tc_wait_ld();
-                    if (n < P.N) {
-                        #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (c + j < live) store_y(P, m0 + c + j, n, v[j]);
-                    }
-                }
-            } else {
-                const int cpr = (P.xcap + P.split - 1) / P.split;   // columns a rank adds
-                const uint32_t mine = smem_addr(red + rank * cpr * 128 + row);
-                int dest = 0, at = 0;
-                #pragma unroll 1
-                for (int c = 0; c < live; c += 8) {
-                    float v[8];
-                    tc_ld_cols<8>(d + c, v);
-                    tc_wait_ld();
+    }
+    const int quad = warp & 3, row = 32 * quad + lane;
+    const int64_t n = static_cast<int64_t>(tn) * 128 + row;
+    const uint32_t d = tmem + (uint32_t(32 * quad) << 16);
+    if (warp >= 2 && warp < 6 && all_lanes(wait_or_abort(&S.d_full, 0, &S.abort_flag, P.err))) {
+        tc_fence_after();
+        if (P.split == 1) {
+            #pragma unroll 1
+            for (int c = 0; c < live; c += 8) {
+                float v[8];
+                tc_ld_cols<8>(d + c, v);
+                tc_wait_ld();
+                if (n < P.N) {
                     #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        if (c + j < live)
-                            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote_addr(mine + at * 512, dest)), "f"(v[j])
-                                         : "memory");
-                        if (++at == cpr) { at = 0; ++dest; }
-                    }
+                    for (int j = 0; j < 8; ++j)
+                        if (c + j < live) store_y(P, c + j, n, v[j]);
                 }
-                asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                __syncwarp();
-                if (lane < P.split)
-                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                                     remote_addr(smem_addr(&S.red_full), lane))
-                                 : "memory");
-                if (rank * cpr < live && wait_or_abort<true>(&S.red_full, 0, &S.abort_flag, P.err) && n < P.N) {
-                    #pragma unroll 1
-                    for (int c = rank * cpr; c < live && c < (rank + 1) * cpr; ++c) {
-                        const float *p = red + (c - rank * cpr) * 128 + row;
-                        float v = 0.f;
-                        for (int q = 0; q < P.split; ++q) v += p[q * cpr * 128];
-                        store_y(P, m0 + c, n, v);
-                    }
+            }
+        } else {
+            const int cpr = (P.xcap + P.split - 1) / P.split;   // columns a rank adds
+            const uint32_t mine = smem_addr(red + rank * cpr * 128 + row);
+            int dest = 0, at = 0;
+            #pragma unroll 1
+            for (int c = 0; c < live; c += 8) {
+                float v[8];
+                tc_ld_cols<8>(d + c, v);
+                tc_wait_ld();
+                #pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (c + j < live)
+                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote_addr(mine + at * 512, dest)), "f"(v[j])
+                                     : "memory");
+                    if (++at == cpr) { at = 0; ++dest; }
+                }
+            }
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            __syncwarp();
+            if (lane < P.split)
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                                 remote_addr(smem_addr(&S.red_full), lane))
+                             : "memory");
+            if (rank * cpr < live && wait_or_abort<true>(&S.red_full, 0, &S.abort_flag, P.err) && n < P.N) {
+                #pragma unroll 1
+                for (int c = rank * cpr; c < live && c < (rank + 1) * cpr; ++c) {
+                    const float *p = red + (c - rank * cpr) * 128 + row;
+                    float v = 0.f;
+                    for (int q = 0; q < P.split; ++q) v += p[q * cpr * 128];
+                    store_y(P, c, n, v);
                 }
             }
         }
@@ -302,8 +300,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
         tc_fence_after();
         tmem_dealloc(tmem, kSplitTmemCols);
     }
-    if (P.split > 1)   // no CTA leaves while another of the cluster may still reach its shared memory
-        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (P.split > 1) cluster_sync_all();   // no CTA leaves while another of the cluster may still reach its shared memory
 }
 
 // Shared memory of a CTA: alone on an SM, one of two, and the least it asks
@@ -314,32 +311,39 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
 // another cluster that waits for it.
 constexpr int kSplitSmemMax = 220 * 1024, kSplitSmemHalf = 111 * 1024, kSplitSmemMin = 80 * 1024;
 
-cudaError_t launch_split(const uint8_t *W, const uint8_t *X, void *Y, bool bf16, int64_t M, int64_t N, int kt,
+cudaError_t launch_split(const uint8_t *W, const uint8_t *X, void *Y, bool bf16, int64_t M, int64_t N, int64_t kt64,
                          const q4::DeviceInfo &dev, cudaStream_t s) {
     static q4::DeviceOnce configured;
     cudaError_t e = configured.run(dev.device, [] {
         return cudaFuncSetAttribute(mx_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitSmemMax);
     });
     if (e != cudaSuccess) return e;
-    SplitParams p{W, X, Y, dev.err, M, N, kt, static_cast<int>(q4::mx_row_tiles(N)), 1, 1, 0, bf16};
-    p.xcap = static_cast<int>((M < 128 ? M : 128) + 7) & ~7;
-    const int64_t tiles = p.tiles_n * q4::mx_row_tiles(M);
-    // SPLIT RULE
-    int split = 1;
-    while (split < 8 && split < kt && tiles * (split + 1) <= 2 * dev.sm_count) ++split;
-    p.split = split;
-    const int budget = tiles * split <= dev.sm_count ? kSplitSmemMax : kSplitSmemHalf;
-    const int need = (kt + split - 1) / split;
-    int slots = (budget - 1024 - split_red_bytes(p.xcap, split)) / split_slot_bytes(p.xcap);
-    if (slots > (kSplitTmemCols - split_d_cols(p.xcap)) / 16) slots = (kSplitTmemCols - split_d_cols(p.xcap)) / 16;
+    const int kt = static_cast<int>(kt64), xcap = static_cast<int>(M + 7) & ~7;
+    const int64_t tiles = q4::mx_row_tiles(N);
+    // K is split into as many parts as leave each CTA an SM of its own, with
+    // four steps or more a part: below, meeting in shared memory (0.5 us) costs more than it
+    // saves.  Measured, us: 1 x 5120 x 8192 11.1 whole, 8.6 in 2, 7.3 in 3
+    // (the rule), 8.3 in 4; 2 x 5120 x 4096 7.2, 6.4, 5.8, 6.0; 4 x 2048 x 8192
+    // 11.2 whole, 5.0 in 8 (the rule); 32 x 16384 x 5120 10.5 whole (the rule),
+    // 13.5 in 2; 1 x 1024 x 1024 2.8 whole (the rule), 3.3 in 4.
+    int split = static_cast<int>(dev.sm_count / tiles);
+    if (split > kt / 4) split = kt / 4;
+    if (split > 8) split = 8;
+    if (split < 1) split = 1;
+    // a CTA that has its SM to itself takes the memory of two; split ones leave
+    // room for the next launch's CTAs
+    const int budget = split == 1 && tiles <= dev.sm_count ? kSplitSmemMax : kSplitSmemHalf;
+    const int need = (kt + split - 1) / split, red = split_red_bytes(xcap, split);
+    int slots = (budget - 1024 - red) / split_slot_bytes(xcap);
+    if (slots > (kSplitTmemCols - split_d_cols(xcap)) / 16) slots = (kSplitTmemCols - split_d_cols(xcap)) / 16;
     if (slots > kMaxSlots) slots = kMaxSlots;
     if (slots > need) slots = need;
-    p.slots = slots < 1 ? 1 : slots;
+    const SplitParams p{W, X, Y, dev.err, N, static_cast<int>(M), kt, split, slots, xcap, bf16};
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = 1024 + p.slots * split_slot_bytes(p.xcap) + split_red_bytes(p.xcap, split);
+    cfg.dynamicSmemBytes = 1024 + slots * split_slot_bytes(xcap) + red;
     if (cfg.dynamicSmemBytes < kSplitSmemMin) cfg.dynamicSmemBytes = kSplitSmemMin;
     cfg.stream = s;
     cfg.attrs = attr;
@@ -374,25 +378,32 @@ struct alignas(64) PairParams {
     unsigned *err;
     int64_t M, N;
     int kt, wt, xt;           // 256-k steps, 128-row tiles of W and of X
-    int tiles_n, tiles_m, tiles;   // tiles of 256 x 256: along N, along M, in all
+    int tiles_n, tiles_m, tiles;   // tiles of 256 x XN: along N, along M, in all
 };
 
 constexpr int kPairThreads = 384;
-constexpr int kPairSlots = 6;
-constexpr int kPairSlotBytes = kMxTileBytes + kMxCodeBytes + 2048;   // W tile, X codes, X scales of both halves
-constexpr int kPairSfCols = 24;                                      // per slot: 8 for W, 16 for X
-static_assert(256 + kPairSlots * kPairSfCols <= 512, "tensor memory");
 
+// XN: activation rows of a tile, 256 or 128
+template <int XN>
+struct Pair {
+    static constexpr int kXCodes = XN / 2 * 128;        // a CTA's half of the rows
+    static constexpr int kXScales = XN / 128 * 1024;    // both CTAs need those of all rows
+    static constexpr int kSlotBytes = kMxTileBytes + kXCodes + kXScales;
+    static constexpr int kSlots = XN == 256 ? 6 : 8;
+    static constexpr int kSfCols = 8 + XN / 16;         // tensor-memory columns of a slot's scales
+    static constexpr int kSmemBytes = kSlots * kSlotBytes + 1024;
+    static_assert(XN + kSlots * kSfCols <= 512, "tensor memory");
+    static_assert(kSmemBytes + 256 <= 232448, "shared memory");
+};
+
+constexpr int kPairMaxSlots = 8;
 struct PairSmem {
-    uint64_t full[kPairSlots], empty[kPairSlots];
+    uint64_t full[kPairMaxSlots], empty[kPairMaxSlots];
     uint64_t d_full, d_empty, mma_done;
     uint32_t tmem_base;
     int abort_flag;
 };
 
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // Says that this warp has read its part of the accumulator.  Relaxed: what it
 // read is in registers (tcgen05.wait::ld), it hands over no memory, and a
 // release would wait for the last tile's stores of Y.
@@ -424,7 +435,7 @@ __device__ __forceinline__ TilePlace place_of(const PairParams &P, int t) {
 // each tile, once the slot is free; `bytes` land in each CTA.  A tile past the
 // last of W or X is the last one again, for rows or columns that are not
 // stored.
-template <class Copy>
+template <int SLOTS, class Copy>
 __device__ __forceinline__ void produce(const PairParams &P, PairSmem &S, int first, int step, int rank, int bytes, Copy &&copy) {
     if ((threadIdx.x & 31) != 0) return;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -434,18 +445,19 @@ __device__ __forceinline__ void produce(const PairParams &P, PairSmem &S, int fi
         const TilePlace at = place_of(P, t);
         for (int i = 0; i < P.kt; ++i, ++issued) {
             if (!wait_or_abort(&S.empty[s], parity, &S.abort_flag, P.err)) {
-                if (rank == 0) drain(S.full, kPairSlots, issued, P.err);
+                if (rank == 0) drain(S.full, SLOTS, issued, P.err);
                 return;
             }
             if (rank == 0) mbar_arrive_expect_tx(&S.full[s], 2 * bytes);
             copy(at, s, i, remote_addr(smem_addr(&S.full[s]), 0));
-            if (++s == kPairSlots) { s = 0; parity ^= 1; }
+            if (++s == SLOTS) { s = 0; parity ^= 1; }
         }
     }
 }
 
-template <bool BF16>
+template <bool BF16, int XN>
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_pair_kernel(const __grid_constant__ PairParams P) {
+    using C = Pair<XN>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ PairSmem S;
     uint8_t *const ring = align_smem<1024>(smem_raw);
@@ -454,7 +466,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
     const int first = static_cast<int>(blockIdx.x) >> 1, step = static_cast<int>(gridDim.x) >> 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kPairSlots; ++s) {
+        for (int s = 0; s < C::kSlots; ++s) {
             mbar_init(&S.full[s], 3);   // the first CTA's producers, which answer for both CTAs' bytes
             mbar_init(&S.empty[s], 1);
         }
@@ -473,26 +485,26 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
     const uint32_t tmem = S.tmem_base;
 
     if (warp == 0) {
-        produce(P, S, first, step, rank, kMxTileBytes, [&](const TilePlace &at, int s, int i, uint32_t bar) {
-            tma_load_pair(smem_addr(ring) + s * kPairSlotBytes, &P.map_w, 17 * (min(2 * at.n + rank, P.wt - 1) * P.kt + i), bar);
+        produce<C::kSlots>(P, S, first, step, rank, kMxTileBytes, [&](const TilePlace &at, int s, int i, uint32_t bar) {
+            tma_load_pair(smem_addr(ring) + s * C::kSlotBytes, &P.map_w, 17 * (min(2 * at.n + rank, P.wt - 1) * P.kt + i), bar);
         });
     } else if (warp == 10) {
-        produce(P, S, first, step, rank, kMxCodeBytes, [&](const TilePlace &at, int s, int i, uint32_t bar) {
-            tma_load_pair(smem_addr(ring) + s * kPairSlotBytes + kMxTileBytes, &P.map_x,
-                          17 * (min(2 * at.m + rank, P.xt - 1) * P.kt + i), bar);
+        produce<C::kSlots>(P, S, first, step, rank, C::kXCodes, [&](const TilePlace &at, int s, int i, uint32_t bar) {
+            const int y = XN == 256 ? 17 * (min(2 * at.m + rank, P.xt - 1) * P.kt + i) : 17 * (at.m * P.kt + i) + 8 * rank;
+            tma_load_pair(smem_addr(ring) + s * C::kSlotBytes + kMxTileBytes, &P.map_x, y, bar);
         });
     } else if (warp == 11) {
-        produce(P, S, first, step, rank, 2048, [&](const TilePlace &at, int s, int i, uint32_t bar) {
+        produce<C::kSlots>(P, S, first, step, rank, C::kXScales, [&](const TilePlace &at, int s, int i, uint32_t bar) {
             #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                tma_load_pair(smem_addr(ring) + s * kPairSlotBytes + kMxTileBytes + kMxCodeBytes + 1024 * h, &P.map_xs,
-                              17 * (min(2 * at.m + h, P.xt - 1) * P.kt + i) + 16, bar);
+            for (int h = 0; h < XN / 128; ++h)
+                tma_load_pair(smem_addr(ring) + s * C::kSlotBytes + kMxTileBytes + C::kXCodes + 1024 * h, &P.map_xs,
+                              17 * (min(XN / 128 * at.m + h, P.xt - 1) * P.kt + i) + 16, bar);
         });
     } else if (warp == 1 && rank == 1) {
         // the first CTA's last commit arrives here too, before this CTA may leave
         wait_or_abort(&S.mma_done, 0, &S.abort_flag, P.err) || mbar_wait(&S.mma_done, 0, P.err);
     } else if (warp == 1) {
-        constexpr uint32_t idesc = mxf4_idesc(256, 256, 0);
+        constexpr uint32_t idesc = mxf4_idesc(256, XN, 0);
         int s = 0;
         uint32_t parity = 0, dpar = 1;
         bool ok = true;
@@ -502,27 +514,27 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
             for (int i = 0; i < P.kt; ++i) {
                 if (!(ok = all_lanes(wait_or_abort(&S.full[s], parity, &S.abort_flag, P.err)))) break;
                 tc_fence_after();
-                const uint32_t base = smem_addr(ring) + s * kPairSlotBytes;
-                const uint32_t sfa = tmem + 256 + kPairSfCols * s, sfb = sfa + 8;
+                const uint32_t base = smem_addr(ring) + s * C::kSlotBytes;
+                const uint32_t sfa = tmem + XN + C::kSfCols * s, sfb = sfa + 8;
                 const uint64_t a = sw128_kmajor_desc(base), b = sw128_kmajor_desc(base + kMxTileBytes);
-                const uint64_t da = scales_desc(base + kMxCodeBytes), db = scales_desc(base + kMxTileBytes + kMxCodeBytes);
+                const uint64_t da = scales_desc(base + kMxCodeBytes), db = scales_desc(base + kMxTileBytes + C::kXCodes);
                 __syncwarp();
                 if (elect_one()) {
                     #pragma unroll
                     for (int g = 0; g < 2; ++g) {   // 512 bytes on: 32 in the descriptor's units
                         tc_cp_scales_pair(sfa + 4 * g, da + 32 * g);
-                        tc_cp_scales_pair(sfb + 8 * g, db + 32 * g);
-                        tc_cp_scales_pair(sfb + 8 * g + 4, db + 64 + 32 * g);
+                        #pragma unroll
+                        for (int h = 0; h < XN / 128; ++h) tc_cp_scales_pair(sfb + XN / 32 * g + 4 * h, db + 64 * h + 32 * g);
                     }
                     #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         tc_mma_mxf4_pair(tmem, a + 2 * j, b + 2 * j, idesc | ((j & 1) ? mxf4_idesc(0, 0, 2) : 0u),
-                                         sfa + 4 * (j >> 1), sfb + 8 * (j >> 1), (i | j) != 0);
+                                         sfa + 4 * (j >> 1), sfb + XN / 32 * (j >> 1), (i | j) != 0);
                     tc_commit_pair(&S.empty[s]);
                     if (i == P.kt - 1) tc_commit_pair(&S.d_full);
                 }
                 __syncwarp();
-                if (++s == kPairSlots) { s = 0; parity ^= 1; }
+                if (++s == C::kSlots) { s = 0; parity ^= 1; }
             }
         }
         // every MMA issued so far has completed once this commit arrives
@@ -530,36 +542,36 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
         __syncwarp();
         wait_or_abort(&S.mma_done, 0, &S.abort_flag, P.err) || mbar_wait(&S.mma_done, 0, P.err);
     } else {
-        const int quad = warp & 3, half = (warp - 2) >> 2;   // lanes [32 quad, +32), columns [128 half, +128)
+        const int quad = warp & 3, half = (warp - 2) >> 2;   // lanes [32 quad, +32), columns [XN/2 half, +XN/2)
         uint32_t parity = 0;
         for (int t = first; t < P.tiles; t += step, parity ^= 1) {
-            if (!wait_or_abort(&S.d_full, parity, &S.abort_flag, P.err)) break;
+            if (!all_lanes(wait_or_abort(&S.d_full, parity, &S.abort_flag, P.err))) break;
             tc_fence_after();
-            float v[4][32];
+            float v[XN / 64][32];
             #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                tc_ld_cols<32>(tmem + (uint32_t(32 * quad) << 16) + 128 * half + 32 * c, v[c]);
+            for (int c = 0; c < XN / 64; ++c)
+                tc_ld_cols<32>(tmem + (uint32_t(32 * quad) << 16) + XN / 2 * half + 32 * c, v[c]);
             tc_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_remote(&S.d_empty, 0);
             const TilePlace at_tile = place_of(P, t);
             const int64_t n = static_cast<int64_t>(2 * at_tile.n + rank) * 128 + 32 * quad + lane;
-            const int64_t m = static_cast<int64_t>(at_tile.m) * 256 + 128 * half;
+            const int64_t m = static_cast<int64_t>(at_tile.m) * XN + XN / 2 * half;
             if (n < P.N && m < P.M) {
                 // whole tiles without a test for each row: with one, storing a
                 // tile took longer (9600 cycles) than the MMAs of 18 steps
                 using T = typename std::conditional<BF16, __nv_bfloat16, float>::type;
                 T *y = static_cast<T *>(P.Y) + m * P.N + n;
-                const int live = static_cast<int>(P.M - m < 128 ? P.M - m : 128);
-                if (live == 128) {
+                const int live = static_cast<int>(P.M - m < XN / 2 ? P.M - m : XN / 2);
+                if (live == XN / 2) {
                     #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < XN / 64; ++c)
                         #pragma unroll
                         for (int j = 0; j < 32; ++j, y += P.N) put(y, v[c][j]);
                 } else {
                     #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < XN / 64; ++c)
                         #pragma unroll
                         for (int j = 0; j < 32; ++j, y += P.N)
                             if (32 * c + j < live) put(y, v[c][j]);
@@ -578,13 +590,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
     cluster_sync_all();
 }
 
-template <bool BF16>
-cudaError_t launch_pair(const PairParams &p, const q4::DeviceInfo &dev, cudaStream_t s) {
-    constexpr int bytes = kPairSlots * kPairSlotBytes + 1024;
+template <bool BF16, int XN>
+cudaError_t launch_pair(PairParams &p, const q4::DeviceInfo &dev, cudaStream_t s) {
+    constexpr int bytes = Pair<XN>::kSmemBytes;
     static q4::DeviceOnce configured;
     static q4::DeviceValue resident;
     const cudaError_t e = configured.run(dev.device, [] {
-        return cudaFuncSetAttribute(mx_pair_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        return cudaFuncSetAttribute(mx_pair_kernel<BF16, XN>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
@@ -606,12 +618,12 @@ cudaError_t launch_pair(const PairParams &p, const q4::DeviceInfo &dev, cudaStre
         c.stream = nullptr;
         c.attrs = &cl;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<BF16>, &c) != cudaSuccess) n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<BF16, XN>, &c) != cudaSuccess) n = 0;
         (void)cudaGetLastError();
         return n > 0 ? n : dev.sm_count / 2;
     });
     cfg.gridDim = dim3(2 * (p.tiles < pairs ? p.tiles : pairs));
-    return cudaLaunchKernelEx(&cfg, mx_pair_kernel<BF16>, p);
+    return cudaLaunchKernelEx(&cfg, mx_pair_kernel<BF16, XN>, p);
 }
 
 }  // namespace
@@ -622,12 +634,20 @@ cudaError_t launch_mx_gemm(const uint8_t *W, const uint8_t *X, void *Y, int y_ty
                            const DeviceInfo &dev, cudaStream_t s) {
     const int64_t kt = mx_k_tiles(K), wt = mx_row_tiles(N), xt = mx_row_tiles(M);
     const bool bf16 = y_type == Q4_TYPE_BF16;
-    if (M <= 128) return launch_split(W, X, Y, bf16, M, N, static_cast<int>(kt), dev, s);
-    const int64_t tiles_n = (wt + 1) / 2, tiles = tiles_n * ((xt + 1) / 2);
-    if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
-    if (17 * wt * kt > 0x7fffffff || 17 * xt * kt > 0x7fffffff) return cudaErrorInvalidValue;
+    // up to 32 rows the weight stream paces both kernels, and splitting K uses
+    // more SMs; above, the pair kernel is ahead (us, split and pair: 16 x 16384
+    // x 5120 9.7 and 10.8, 32 x 16384 x 5120 10.9 and 10.8, 64 x 16384 x 5120
+    // 12.4 and 10.9, 16 x 5120 x 8192 8.4 and 11.1, 64 x 5120 x 8192 12.7 and 11.3)
+    if (M <= 32) return launch_split(W, X, Y, bf16, M, N, kt, dev, s);
+    const int64_t tiles_n = (wt + 1) / 2;
+    // tiles of 128 activation rows while they all run at once, of 256 beyond
+    // (us, 128 and 256: 333 x 5003 x 4128 9.0 and 11.3, 512 x 2048 x 2048 6.2 and
+    // 7.9; 256 x 16384 x 5120 15.9 and 13.6, 600 x 5120 x 4096 12.6 and 11.3)
+    const bool wide = tiles_n * xt > dev.sm_count / 2;
+    const int64_t tiles_m = wide ? (xt + 1) / 2 : xt, tiles = tiles_n * tiles_m;
+    if (tiles > 0x7fffffff || 17 * wt * kt > 0x7fffffff || 17 * xt * kt > 0x7fffffff) return cudaErrorInvalidValue;
     PairParams p;
-    if (!encode_1k_rows_map(&p.map_w, W, 17 * wt * kt, 17) || !encode_1k_rows_map(&p.map_x, X, 17 * xt * kt, 16) ||
+    if (!encode_1k_rows_map(&p.map_w, W, 17 * wt * kt, 17) || !encode_1k_rows_map(&p.map_x, X, 17 * xt * kt, wide ? 16 : 8) ||
         !encode_1k_rows_map(&p.map_xs, X, 17 * xt * kt, 1))
         return cudaErrorInvalidValue;
     p.Y = Y;
@@ -638,9 +658,10 @@ cudaError_t launch_mx_gemm(const uint8_t *W, const uint8_t *X, void *Y, int y_ty
     p.wt = static_cast<int>(wt);
     p.xt = static_cast<int>(xt);
     p.tiles_n = static_cast<int>(tiles_n);
-    p.tiles_m = static_cast<int>((xt + 1) / 2);
+    p.tiles_m = static_cast<int>(tiles_m);
     p.tiles = static_cast<int>(tiles);
-    return bf16 ? launch_pair<true>(p, dev, s) : launch_pair<false>(p, dev, s);
+    if (wide) return bf16 ? launch_pair<true, 256>(p, dev, s) : launch_pair<false, 256>(p, dev, s);
+    return bf16 ? launch_pair<true, 128>(p, dev, s) : launch_pair<false, 128>(p, dev, s);
 }
 
 }  // namespace q4

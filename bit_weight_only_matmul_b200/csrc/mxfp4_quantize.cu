@@ -2,12 +2,18 @@
 // checkpoint's codes and scales into the library's layout.  All three are one
 // pass over memory.
 //
-// A warp takes eight consecutive rows of a tile (256 k, 8 values a lane, four
-// lanes a block).  It reads 512 or 1024 contiguous bytes of each row, all rows
-// before it works on the first (one row at a time kept too little in flight:
-// 4096 x 5120 bf16 19.5 us), finds each block's largest magnitude with two
+// A warp takes two or eight consecutive rows of a tile (256 k, 8 values a
+// lane, four lanes a block).  It reads 512 or 1024 contiguous bytes of each
+// row, all rows before it works on the first, finds each block's largest magnitude with two
 // shuffles, and writes each row's 128 bytes of codes as one line and its
 // eight scale bytes from eight lanes.
+//
+// Bound by HBM.  Eight rows a warp keep more in flight where there are warps
+// enough (8192 x 8192 bf16 quantize 35.7 us against 39.9 with two rows, dequant
+// of 16384 x 5120 to bf16 35.1 against 44.2); two spread few rows over the SMs
+// (1003 x 4128 fp16 quantize 4.3 us against 5.9), and are enough for fp32,
+// whose rows are twice as many bytes (16384 x 5120 quantize 57.8 against 59.0 us,
+// dequant 64.0 against 72.5).
 #include "mxfp4_layout.cuh"
 
 namespace {
@@ -15,10 +21,9 @@ namespace {
 using namespace q4dev;
 using q4::kMxTileBytes;
 
-constexpr int kRows = 8;        // rows a warp takes
 constexpr int kWarps = 4;       // warps of a CTA
 
-// A warp's part of the matrix: rows row0 .. row0 + rows - 1 of tile column t.
+// A warp's part of the matrix, ROWS rows or the last few: rows row0 .. row0 + rows - 1 of tile column t.
 struct Part {
     int64_t row0, k;   // k: the lane's first value
     int rows, r;       // r: row0's place in its tile
@@ -26,13 +31,14 @@ struct Part {
     bool live;         // the lane's values lie within K
 };
 
+template <int ROWS>
 __device__ __forceinline__ bool part_of(Part &p, const uint8_t *W, int64_t R, int64_t K, int kt) {
     const int lane = threadIdx.x & 31;
     const uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const uint32_t g = u / static_cast<uint32_t>(kt), t = u - g * kt;
-    p.row0 = static_cast<int64_t>(g) * kRows;
+    p.row0 = static_cast<int64_t>(g) * ROWS;
     if (p.row0 >= R) return false;
-    p.rows = R - p.row0 < kRows ? static_cast<int>(R - p.row0) : kRows;
+    p.rows = R - p.row0 < ROWS ? static_cast<int>(R - p.row0) : ROWS;
     p.r = static_cast<int>(p.row0 & 127);
     p.tile = const_cast<uint8_t *>(W) + ((p.row0 >> 7) * kt + t) * kMxTileBytes;
     p.k = static_cast<int64_t>(t) * 256 + 8 * lane;
@@ -52,20 +58,20 @@ __device__ __forceinline__ uint32_t *scale_word(const Part &p, int lane) {
     return reinterpret_cast<uint32_t *>(p.tile + mx_scale_offset(p.r + (lane >> 1), lane & 1));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 8 : 5)
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(32 * kWarps, 8)
     mx_quantize_kernel(const T *__restrict__ X, uint8_t *__restrict__ W, int64_t R, int64_t K, int kt) {
     begin_dependent();
     const int lane = threadIdx.x & 31;
     Part p;
-    if (!part_of(p, W, R, K, kt)) return;
+    if (!part_of<ROWS>(p, W, R, K, kt)) return;
     const int64_t at = p.row0 * K + p.k;
-    Raw8<T> x[kRows];
+    Raw8<T> x[ROWS];
     #pragma unroll
-    for (int i = 0; i < kRows; ++i)
+    for (int i = 0; i < ROWS; ++i)
         if (p.live && i < p.rows) x[i].load(X, at + i * K);
     #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
         if (i < p.rows) {   // the same in all lanes
             float v[8] = {};
             if (p.live) x[i].get(v);
@@ -110,20 +116,20 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
     return __uint_as_float(__float_as_uint(m) | ((c & 8u) << 28));
 }
 
-template <typename T>
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(32 * kWarps) mx_dequant_kernel(const uint8_t *__restrict__ W, T *__restrict__ out, int64_t R,
                                                                  int64_t K, int kt) {
     begin_dependent();
     const int lane = threadIdx.x & 31;
     Part p;
-    if (!part_of(p, W, R, K, kt)) return;
-    uint32_t code[kRows];
+    if (!part_of<ROWS>(p, W, R, K, kt)) return;
+    uint32_t code[ROWS];
     #pragma unroll
-    for (int i = 0; i < kRows; ++i) code[i] = i < p.rows ? __ldcs(code_word(p, i, lane)) : 0u;
+    for (int i = 0; i < ROWS; ++i) code[i] = i < p.rows ? __ldcs(code_word(p, i, lane)) : 0u;
     const uint32_t words = lane < 2 * p.rows ? __ldcs(scale_word(p, lane)) : 0u;
     T *o = out + p.row0 * K + p.k;
     #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
         const uint32_t word = __shfl_sync(0xffffffffu, words, 2 * i + (lane >> 4));
         if (i < p.rows && p.live) {
             const float s = mx_scale((word >> (8 * ((lane >> 2) & 3))) & 255u);
@@ -135,15 +141,16 @@ __global__ void __launch_bounds__(32 * kWarps) mx_dequant_kernel(const uint8_t *
     }
 }
 
+template <int ROWS>
 __global__ void __launch_bounds__(32 * kWarps) mx_pack_kernel(const uint8_t *__restrict__ codes,
                                                               const uint8_t *__restrict__ scales, uint8_t *__restrict__ W,
                                                               int64_t R, int64_t K, int kt) {
     begin_dependent();
     const int lane = threadIdx.x & 31;
     Part p;
-    if (!part_of(p, W, R, K, kt)) return;
+    if (!part_of<ROWS>(p, W, R, K, kt)) return;
     #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
         if (i < p.rows) {
             const int64_t at = (p.row0 + i) * K + p.k;
             *code_word(p, i, lane) = p.live ? __ldcs(reinterpret_cast<const uint32_t *>(codes + at / 2)) : 0u;
@@ -152,22 +159,27 @@ __global__ void __launch_bounds__(32 * kWarps) mx_pack_kernel(const uint8_t *__r
     }
 }
 
-// CTAs of a pass over R rows in kt tile columns; 0 if they do not fit a grid
-// (no device memory holds such a matrix).
-int64_t grid_for(int64_t R, int64_t kt) {
-    const int64_t parts = (R + kRows - 1) / kRows * kt;
+// CTAs of a pass over R rows in kt tile columns, `rows` rows a warp; 0 if they
+// do not fit a grid (no device memory holds such a matrix).
+int64_t grid_for(int64_t R, int64_t kt, int rows) {
+    const int64_t parts = (R + rows - 1) / rows * kt;
     return parts > 0x7fffffff ? 0 : (parts + kWarps - 1) / kWarps;
 }
 
-template <typename T>
-cudaError_t quantize(const void *X, uint8_t *W, int64_t R, int64_t K, int64_t kt, cudaStream_t s) {
-    return launch_dependent(mx_quantize_kernel<T>, grid_for(R, kt), 32 * kWarps, s, static_cast<const T *>(X), W, R, K,
-                            static_cast<int>(kt));
+// Eight rows a warp where that leaves every SM as many warps as it holds.
+bool eight_rows(int type, int64_t R, int64_t kt, const q4::DeviceInfo &dev) {
+    return type != Q4_TYPE_F32 && R / 8 * kt >= 64LL * dev.sm_count;
 }
 
-template <typename T>
+template <typename T, int ROWS>
+cudaError_t quantize(const void *X, uint8_t *W, int64_t R, int64_t K, int64_t kt, cudaStream_t s) {
+    return launch_dependent(mx_quantize_kernel<T, ROWS>, grid_for(R, kt, ROWS), 32 * kWarps, s, static_cast<const T *>(X), W,
+                            R, K, static_cast<int>(kt));
+}
+
+template <typename T, int ROWS>
 cudaError_t dequant(const uint8_t *W, void *out, int64_t R, int64_t K, int64_t kt, cudaStream_t s) {
-    return launch_dependent(mx_dequant_kernel<T>, grid_for(R, kt), 32 * kWarps, s, W, static_cast<T *>(out), R, K,
+    return launch_dependent(mx_dequant_kernel<T, ROWS>, grid_for(R, kt, ROWS), 32 * kWarps, s, W, static_cast<T *>(out), R, K,
                             static_cast<int>(kt));
 }
 
@@ -175,23 +187,27 @@ cudaError_t dequant(const uint8_t *W, void *out, int64_t R, int64_t K, int64_t k
 
 namespace q4 {
 
-cudaError_t launch_mx_quantize(const void *X, int type, uint8_t *W, int64_t R, int64_t K, cudaStream_t s) {
+cudaError_t launch_mx_quantize(const void *X, int type, uint8_t *W, int64_t R, int64_t K, const DeviceInfo &dev,
+                               cudaStream_t s) {
     const int64_t kt = mx_k_tiles(K);
-    return type == Q4_TYPE_F32    ? quantize<float>(X, W, R, K, kt, s)
-           : type == Q4_TYPE_BF16 ? quantize<__nv_bfloat16>(X, W, R, K, kt, s)
-                                  : quantize<__half>(X, W, R, K, kt, s);
+    if (type == Q4_TYPE_F32) return quantize<float, 2>(X, W, R, K, kt, s);
+    if (eight_rows(type, R, kt, dev))
+        return type == Q4_TYPE_BF16 ? quantize<__nv_bfloat16, 8>(X, W, R, K, kt, s) : quantize<__half, 8>(X, W, R, K, kt, s);
+    return type == Q4_TYPE_BF16 ? quantize<__nv_bfloat16, 2>(X, W, R, K, kt, s) : quantize<__half, 2>(X, W, R, K, kt, s);
 }
 
-cudaError_t launch_mx_dequant(const uint8_t *W, void *out, int type, int64_t R, int64_t K, cudaStream_t s) {
+cudaError_t launch_mx_dequant(const uint8_t *W, void *out, int type, int64_t R, int64_t K, const DeviceInfo &dev,
+                              cudaStream_t s) {
     const int64_t kt = mx_k_tiles(K);
-    return type == Q4_TYPE_F32    ? dequant<float>(W, out, R, K, kt, s)
-           : type == Q4_TYPE_BF16 ? dequant<__nv_bfloat16>(W, out, R, K, kt, s)
-                                  : dequant<__half>(W, out, R, K, kt, s);
+    if (type == Q4_TYPE_F32) return dequant<float, 2>(W, out, R, K, kt, s);
+    if (eight_rows(type, R, kt, dev))
+        return type == Q4_TYPE_BF16 ? dequant<__nv_bfloat16, 8>(W, out, R, K, kt, s) : dequant<__half, 8>(W, out, R, K, kt, s);
+    return type == Q4_TYPE_BF16 ? dequant<__nv_bfloat16, 2>(W, out, R, K, kt, s) : dequant<__half, 2>(W, out, R, K, kt, s);
 }
 
 cudaError_t launch_mx_pack(const uint8_t *codes, const uint8_t *scales, uint8_t *W, int64_t R, int64_t K, cudaStream_t s) {
     const int64_t kt = mx_k_tiles(K);
-    return launch_dependent(mx_pack_kernel, grid_for(R, kt), 32 * kWarps, s, codes, scales, W, R, K, static_cast<int>(kt));
+    return launch_dependent(mx_pack_kernel<2>, grid_for(R, kt, 2), 32 * kWarps, s, codes, scales, W, R, K, static_cast<int>(kt));
 }
 
 }  // namespace q4

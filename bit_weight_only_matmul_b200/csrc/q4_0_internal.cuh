@@ -128,8 +128,10 @@ int api_device(const DeviceInfo **out);
 int api_cuda_fail(cudaError_t e);
 
 // MXFP4 (the layout: mxfp4_layout.cuh); types are Q4_TYPE_*.
-cudaError_t launch_mx_quantize(const void *X, int type, uint8_t *W, int64_t R, int64_t K, cudaStream_t s);
-cudaError_t launch_mx_dequant(const uint8_t *W, void *out, int type, int64_t R, int64_t K, cudaStream_t s);
+cudaError_t launch_mx_quantize(const void *X, int type, uint8_t *W, int64_t R, int64_t K, const DeviceInfo &dev,
+                               cudaStream_t s);
+cudaError_t launch_mx_dequant(const uint8_t *W, void *out, int type, int64_t R, int64_t K, const DeviceInfo &dev,
+                              cudaStream_t s);
 cudaError_t launch_mx_pack(const uint8_t *codes, const uint8_t *scales, uint8_t *W, int64_t R, int64_t K, cudaStream_t s);
 cudaError_t launch_mx_gemm(const uint8_t *W, const uint8_t *X, void *Y, int y_type, int64_t M, int64_t N, int64_t K,
                            const DeviceInfo &dev, cudaStream_t s);
