@@ -79,6 +79,19 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
     return r;
 }
 
+// Four of them.
+__device__ __forceinline__ uint32_t e2m1x4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n .reg .b8 b0, b1;\n .reg .b16 h;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+        " mov.b16 h, {b0, b1};\n"
+        " cvt.u32.u16 %0, h;\n}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
 // Four consecutive lanes hold a block, eight values each (lane & 3 the part):
 // the lane's code word; `byte` is the block's scale byte in all four lanes.
 // All 32 lanes of the warp take part.  Multiplying by a power of two is exact

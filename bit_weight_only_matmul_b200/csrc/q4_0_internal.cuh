@@ -286,7 +286,7 @@ __device__ __forceinline__ void begin_dependent() {
 // kernel before is ending, so the kernel must call begin_dependent() before it
 // touches global memory.
 template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t s, A... args) {
+cudaError_t launch_dependent_smem(void (*kernel)(P...), int64_t grid, int threads, size_t smem, cudaStream_t s, A... args) {
     if (grid < 1 || grid > 0x7fffffff) return cudaErrorInvalidValue;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -294,10 +294,15 @@ cudaError_t launch_dependent(void (*kernel)(P...), int64_t grid, int threads, cu
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), int64_t grid, int threads, cudaStream_t s, A... args) {
+    return launch_dependent_smem(kernel, grid, threads, 0, s, args...);
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {

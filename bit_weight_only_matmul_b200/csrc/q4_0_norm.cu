@@ -7,12 +7,20 @@
 //     x  = r' / sqrt(mean(r'^2) + eps) * pre
 //
 // Memory-bound: y and r are read once and r' and x written once, everything
-// in between stays in registers.  A CTA takes a row; a thread holds G groups
-// of eight consecutive values, so that a warp's group is one row of an MXFP4
-// tile (256 k) and x can be written as MXFP4 with the code that
-// mxfp4_quantize uses.  The two sums go through shuffles and one line of
-// shared memory and are added in a fixed order.  All arithmetic is fp32; r'
-// is rounded once to r's type, and x is taken from r' before that rounding.
+// in between stays in registers.  A row belongs to a CTA; a thread holds G
+// groups of eight values, a group being two runs of four, 128 values apart,
+// in the 256 values of its warp: every load and store of a warp is one
+// contiguous piece, and a warp's group is one row of an MXFP4 tile, so that x
+// can be written as MXFP4.  The two sums go through shuffles and one line of
+// shared memory and are added in a fixed order.  All arithmetic is fp32; r' is
+// rounded once to r's type, and x is taken from r' before that rounding.
+//
+// Two kernels.  block_norm_kernel keeps a row's values in registers from the
+// load on: for few rows, where one row's time is all there is.
+// block_norm_many_kernel lands them in shared memory first (each thread copies
+// what it will read itself, so nobody waits for anybody), which leaves room on
+// an SM for twice as many rows: a row's time is mostly waiting, for memory and
+// for its two sums.
 #include "mxfp4_layout.cuh"
 
 namespace {
@@ -23,155 +31,367 @@ struct NormParams {
     const void *y, *r;
     void *r_out, *x;
     const float *post, *gate, *pre;
-    int64_t M, D, gate_span, kt;
+    int64_t M, gate_span;
+    int D, kt;
     float scale, eps;
-    int y_type, r_type, x_type;
+    int x_type;
 };
 
-__device__ __forceinline__ float block_sum(float v, float *part) {
+__device__ __forceinline__ float warp_sum(float v) {
     #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The sum over the CTA, the same bits in all lanes: every warp adds the line
+// itself, in the same order.
+__device__ __forceinline__ float block_sum(float v, float *part, int warps) {
+    v = warp_sum(v);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    // every warp adds the line itself: the same order, the same bits in all lanes
-    float s = (threadIdx.x & 31) < (blockDim.x >> 5) ? part[threadIdx.x & 31] : 0.f;
-    #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
+    return warp_sum((threadIdx.x & 31) < warps ? part[threadIdx.x & 31] : 0.f);
 }
 
-__device__ __forceinline__ void weights8(const float *p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ void quad(float4 a, float (&v)[8], int h) {
+    v[4 * h] = a.x; v[4 * h + 1] = a.y; v[4 * h + 2] = a.z; v[4 * h + 3] = a.w;
 }
 
-__device__ __forceinline__ void store8_any(void *p, int type, int64_t at, const float (&v)[8]) {
-    if (type == Q4_TYPE_F32) {
-        float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
-        q[0] = make_float4(v[0], v[1], v[2], v[3]);
-        q[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        uint32_t w[4];
+// A group as it lies in memory, its first run at `p`; a
+// run past the row's end (low, high: there is a first, a second one) stays zero.
+template <class T> struct Raw;
+template <> struct Raw<float> {
+    float4 q[2];
+    __device__ __forceinline__ void load(const float *p, bool low, bool high) {
+        if (low) q[0] = __ldcs(reinterpret_cast<const float4 *>(p));
+        if (high) q[1] = __ldcs(reinterpret_cast<const float4 *>(p + 128));
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const { quad(q[0], v, 0); quad(q[1], v, 1); }
+};
+template <> struct Raw<__nv_bfloat16> {
+    uint2 q[2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool low, bool high) {
+        if (low) q[0] = __ldcs(reinterpret_cast<const uint2 *>(p));
+        if (high) q[1] = __ldcs(reinterpret_cast<const uint2 *>(p + 128));
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
         #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int h = 0; h < 2; ++h)
+            quad(make_float4(__uint_as_float(q[h].x << 16), __uint_as_float(q[h].x & 0xFFFF0000u),
+                             __uint_as_float(q[h].y << 16), __uint_as_float(q[h].y & 0xFFFF0000u)), v, h);
+    }
+};
+
+__device__ __forceinline__ void load_weights(const float *p, bool low, bool high, float (&v)[8]) {
+    quad(low ? __ldg(reinterpret_cast<const float4 *>(p)) : make_float4(0.f, 0.f, 0.f, 0.f), v, 0);
+    quad(high ? __ldg(reinterpret_cast<const float4 *>(p + 128)) : make_float4(0.f, 0.f, 0.f, 0.f), v, 1);
+}
+
+// One run of a group.
+__device__ __forceinline__ void store_run(float *p, const float *v) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store_run(__nv_bfloat16 *p, const float *v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
+// What a thread does with its G groups of a row.  Column of run h of group j:
+// first + 256 * warps * j + 128 * h.
+template <int G>
+struct Lane {
+    int first, step;   // step: 256 * warps
+    __device__ __forceinline__ Lane(int warp, int lane, int warps) : first(256 * warp + 4 * lane), step(256 * warps) {}
+    __device__ __forceinline__ int column(int j, int h) const { return first + step * j + 128 * h; }
+};
+
+template <int G>
+__device__ __forceinline__ float square_sum(const float (&v)[G][8]) {
+    float ss = 0.f;
+    #pragma unroll
+    for (int j = 0; j < G; ++j)
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+    return ss;
+}
+
+// w = post * gate of a group (1 where one is missing).
+__device__ __forceinline__ void block_weights(const NormParams &P, const float *gate, int k, float (&w)[8]) {
+    const bool low = k < P.D, high = k + 128 < P.D;
+    if (P.post) load_weights(P.post + k, low, high, w);
+    else if (gate) load_weights(gate + k, low, high, w);
+    else {
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    }
+    if (P.post && gate) {
+        float g[8];
+        load_weights(gate + k, low, high, g);
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] *= g[i];
     }
 }
 
-// G: groups of eight values a thread holds; T: threads at most; YT, RT: the
-// types of y and r.
-template <int G, int T, class YT, class RT>
-__global__ void __launch_bounds__(T, G == 2 && T == 512 ? 2 : 1) block_norm_kernel(const __grid_constant__ NormParams P) {
+__device__ __forceinline__ const float *gate_row(const NormParams &P, int64_t row) {
+    return !P.gate ? nullptr : P.gate + (P.gate_span ? row / P.gate_span : 0) * P.D;
+}
+
+// r' of a group from h, its weight and r.
+__device__ __forceinline__ void add_block(float (&h)[8], const float (&w)[8], float fy, const float (&r)[8]) {
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = fmaf(h[i] * w[i], fy, r[i]);
+}
+
+template <int G, class T>
+__device__ __forceinline__ void store_row(void *p, int64_t at, const Lane<G> &L, int D, const float (&v)[G][8]) {
+    T *q = static_cast<T *>(p) + at;
+    #pragma unroll
+    for (int j = 0; j < G; ++j) {
+        const int k = L.column(j, 0);
+        if (k < D) store_run(q + k, v[j]);
+        if (k + 128 < D) store_run(q + k + 128, v[j] + 4);
+    }
+}
+
+// x as one row of an MXFP4 matrix: a block is one run of eight lanes, and whole
+// warps take part (blocks past D: zero codes and a zero scale byte).
+template <int G>
+__device__ __forceinline__ void store_mxfp4(const NormParams &P, int64_t row, const Lane<G> &L, int lane, const float (&v)[G][8]) {
+    const int r = static_cast<int>(row & 127);
+    #pragma unroll
+    for (int j = 0; j < G; ++j) {
+        const int k = L.column(j, 0), tile_k = k >> 8;   // the same in the whole warp
+        if (tile_k >= P.kt) break;
+        uint8_t *tile = static_cast<uint8_t *>(P.x) + ((row >> 7) * P.kt + tile_k) * q4::kMxTileBytes;
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool live = k + 128 * h < P.D;
+            uint32_t a = 0;
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t b = __float_as_uint(v[j][4 * h + i]) & 0x7FFFFFFFu;
+                a = a > b ? a : b;
+            }
+            #pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                const uint32_t b = __shfl_xor_sync(0xffffffffu, a, o);
+                a = a > b ? a : b;
+            }
+            const uint32_t byte = live ? mx_scale_byte(a) : 0u;
+            const float inv = mx_inverse_scale(byte);
+            const float *u = v[j] + 4 * h;
+            const uint32_t code = live ? e2m1x4(u[0] * inv, u[1] * inv, u[2] * inv, u[3] * inv) : 0u;
+            const int b = 4 * h + (lane >> 3);
+            *reinterpret_cast<uint16_t *>(tile + mx_code_offset(r, b) + 2 * (lane & 7)) = static_cast<uint16_t>(code);
+            if ((lane & 7) == 0) tile[mx_scale_offset(r, h) + (lane >> 3)] = static_cast<uint8_t>(byte);
+        }
+    }
+}
+
+template <int G>
+__device__ __forceinline__ void store_x(const NormParams &P, int64_t row, const Lane<G> &L, int lane, const float (&v)[G][8]) {
+    if (P.x_type == Q4_TYPE_MXFP4) store_mxfp4<G>(P, row, L, lane, v);
+    else if (P.x_type == Q4_TYPE_BF16) store_row<G, __nv_bfloat16>(P.x, row * P.D, L, P.D, v);
+    else store_row<G, float>(P.x, row * P.D, L, P.D, v);
+}
+
+// ---------------------------------------------------------------- a row a CTA
+
+// EAGER: the weights are on their way with the rows; where they would not fit
+// in the registers as well they are loaded when they are needed.
+template <int G, int T, bool EAGER, class YT, class RT>
+__global__ void __launch_bounds__(T) block_norm_kernel(const __grid_constant__ NormParams P) {
     __shared__ float part[2][32];
     begin_dependent();
-    const int lane = threadIdx.x & 31;
-    const int D = static_cast<int>(P.D), gap = 8 * blockDim.x;
-    for (int64_t row = blockIdx.x; row < P.M; row += gridDim.x) {
-        const int64_t at = row * P.D;
-        // both rows on their way before the first sum
-        Raw8<YT> y[G];
-        Raw8<RT> r[G];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const Lane<G> L(warp, lane, warps);
+    const int64_t row = blockIdx.x, at = row * P.D;
+    const float *gate = gate_row(P, row);
+    float v[G][8], w[EAGER ? G : 1][8], pre[EAGER ? G : 1][8];
+    Raw<RT> q[G] = {};
+    {
+        Raw<YT> y[G] = {};
         #pragma unroll
         for (int j = 0; j < G; ++j) {
-            const int k = 8 * threadIdx.x + j * gap;
-            if (k < D && P.y) y[j].load(P.y, at + k);
+            const int k = L.column(j, 0);
+            if (P.y) y[j].load(static_cast<const YT *>(P.y) + at + k, k < P.D, k + 128 < P.D);
         }
         #pragma unroll
         for (int j = 0; j < G; ++j) {
-            const int k = 8 * threadIdx.x + j * gap;
-            if (k < D) r[j].load(P.r, at + k);
+            const int k = L.column(j, 0);
+            q[j].load(static_cast<const RT *>(P.r) + at + k, k < P.D, k + 128 < P.D);
         }
-        float fy = P.scale;
-        if (P.y && P.post) {
-            float ss = 0.f;
-            #pragma unroll
-            for (int j = 0; j < G; ++j)
-                if (8 * threadIdx.x + j * gap < D) {
-                    float v[8];
-                    y[j].get(v);
-                    #pragma unroll
-                    for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-                }
-            fy *= rsqrtf(block_sum(ss, part[0]) / static_cast<float>(D) + P.eps);
-        }
-        const float *gate = P.gate ? P.gate + (P.gate_span ? row / P.gate_span : 0) * P.D : nullptr;
-        float v[G][8];   // r'
-        float ss = 0.f;
-        #pragma unroll
-        for (int j = 0; j < G; ++j) {
-            const int k = 8 * threadIdx.x + j * gap;
-            if (k < D) {
-                r[j].get(v[j]);
-                if (P.y) {
-                    float h[8], w[8];
-                    y[j].get(h);
-                    if (P.post) {
-                        weights8(P.post + k, w);
-                        #pragma unroll
-                        for (int i = 0; i < 8; ++i) h[i] *= w[i];
-                    }
-                    if (gate) {
-                        weights8(gate + k, w);
-                        #pragma unroll
-                        for (int i = 0; i < 8; ++i) h[i] *= w[i];
-                    }
-                    #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[j][i] = fmaf(h[i], fy, v[j][i]);
-                }
-                if (P.r_out) store8_any(P.r_out, P.r_type, at + k, v[j]);
-                #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
-            }
-        }
-        if (P.x) {
-            const float fx = rsqrtf(block_sum(ss, part[1]) / static_cast<float>(D) + P.eps);
+        if (EAGER) {
             #pragma unroll
             for (int j = 0; j < G; ++j) {
-                const int k = 8 * threadIdx.x + j * gap;
-                const bool live = k < D;
-                if (live) {
-                    if (P.pre) {
-                        float w[8];
-                        weights8(P.pre + k, w);
-                        #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[j][i] = v[j][i] * fx * w[i];
-                    } else {
-                        #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[j][i] *= fx;
-                    }
-                    if (P.x_type != Q4_TYPE_MXFP4) store8_any(P.x, P.x_type, at + k, v[j]);
-                }
-                if (P.x_type == Q4_TYPE_MXFP4 && (k >> 8) < P.kt) {   // the whole warp: k >> 8 is the warp's tile
-                    if (!live) {
-                        #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
-                    }
-                    uint32_t byte;
-                    const uint32_t code = mx_encode8(v[j], byte);
-                    const uint32_t word = mx_scale_word(live ? byte : 0u, lane);
-                    uint8_t *tile = static_cast<uint8_t *>(P.x) + ((row >> 7) * P.kt + (k >> 8)) * q4::kMxTileBytes;
-                    const int rr = static_cast<int>(row & 127);
-                    *reinterpret_cast<uint32_t *>(tile + mx_code_offset(rr, lane >> 2) + 4 * (lane & 3)) = code;
-                    if ((lane & 15) == 0) *reinterpret_cast<uint32_t *>(tile + mx_scale_offset(rr, lane >> 4)) = word;
-                }
+                const int k = L.column(j, 0);
+                if (P.y) block_weights(P, gate, k, w[j]);
+                if (P.pre) load_weights(P.pre + k, k < P.D, k + 128 < P.D, pre[j]);
             }
         }
-        if (gridDim.x < P.M) __syncthreads();   // the sums' line is written again for the next row
+        #pragma unroll
+        for (int j = 0; j < G; ++j) y[j].get(v[j]);
+    }
+    float fy = P.scale;
+    if (P.y && P.post) fy *= rsqrtf(block_sum(square_sum<G>(v), part[0], warps) / static_cast<float>(P.D) + P.eps);
+    #pragma unroll
+    for (int j = 0; j < G; ++j) {
+        float r[8];
+        q[j].get(r);
+        if (P.y) {
+            if (!EAGER) block_weights(P, gate, L.column(j, 0), w[0]);
+            add_block(v[j], w[EAGER ? j : 0], fy, r);
+        } else {
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] = r[i];
+        }
+    }
+    if (P.r_out) store_row<G, RT>(P.r_out, at, L, P.D, v);
+    if (P.x) {
+        const float fx = rsqrtf(block_sum(square_sum<G>(v), part[1], warps) / static_cast<float>(P.D) + P.eps);
+        #pragma unroll
+        for (int j = 0; j < G; ++j) {
+            const int k = L.column(j, 0);
+            if (!EAGER && P.pre) load_weights(P.pre + k, k < P.D, k + 128 < P.D, pre[0]);
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] = P.pre ? v[j][i] * fx * pre[EAGER ? j : 0][i] : v[j][i] * fx;
+        }
+        store_x<G>(P, row, L, lane, v);
     }
 }
 
-template <int G, int T>
-cudaError_t launch(const NormParams &p, int threads, int64_t grid, cudaStream_t s) {
-    const bool yf = p.y_type == Q4_TYPE_F32, rf = p.r_type == Q4_TYPE_F32;
+// ---------------------------------------------------------------- many rows
+
+// One run of a group from global to shared memory: 16 bytes of fp32, 8 of bf16.
+__device__ __forceinline__ void copy_run(uint32_t dst, const float *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_run(uint32_t dst, const __nv_bfloat16 *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void get_run(const float *p, float *v) {
+    const float4 a = *reinterpret_cast<const float4 *>(p);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+__device__ __forceinline__ void get_run(const __nv_bfloat16 *p, float *v) {
+    const uint2 a = *reinterpret_cast<const uint2 *>(p);
+    v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xFFFF0000u);
+}
+
+// A thread's groups of a row between global memory, shared memory and
+// registers; run (j, h) of thread t at (2j + h) * threads + t.
+template <int G, class T>
+struct Landing {
+    T *mine;
+    int gap;
+    __device__ __forceinline__ Landing(uint8_t *base) : mine(reinterpret_cast<T *>(base) + 4 * threadIdx.x), gap(4 * blockDim.x) {}
+    __device__ __forceinline__ void copy(const T *row, const Lane<G> &L, int D) const {
+        #pragma unroll
+        for (int j = 0; j < G; ++j)
+            #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = L.column(j, h);
+                if (k < D) copy_run(smem_addr(mine + (2 * j + h) * gap), row + k);
+            }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ void get(const Lane<G> &L, int D, int j, float (&v)[8]) const {
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (L.column(j, h) < D) {
+                get_run(mine + (2 * j + h) * gap, v + 4 * h);
+            } else {
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * h + i] = 0.f;
+            }
+        }
+    }
+};
+
+constexpr int kManyThreads = 256;
+
+template <int G, class YT, class RT>
+__global__ void __launch_bounds__(kManyThreads, 3) block_norm_many_kernel(const __grid_constant__ NormParams P) {
+    extern __shared__ __align__(16) uint8_t landing[];
+    __shared__ float part[2][32];
+    begin_dependent();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const Lane<G> L(warp, lane, warps);
+    const int64_t row = blockIdx.x, at = row * P.D;
+    const Landing<G, YT> y(landing);
+    const Landing<G, RT> r(landing + (P.y ? blockDim.x * G * 8 * sizeof(YT) : 0));
+    if (P.y) y.copy(static_cast<const YT *>(P.y) + at, L, P.D);
+    r.copy(static_cast<const RT *>(P.r) + at, L, P.D);
+    const float *gate = gate_row(P, row);
+    float v[G][8];
+    float fy = P.scale;
+    if (P.y) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        #pragma unroll
+        for (int j = 0; j < G; ++j) y.get(L, P.D, j, v[j]);
+        if (P.post) fy *= rsqrtf(block_sum(square_sum<G>(v), part[0], warps) / static_cast<float>(P.D) + P.eps);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    #pragma unroll
+    for (int j = 0; j < G; ++j) {
+        float q[8];
+        r.get(L, P.D, j, q);
+        if (P.y) {
+            float w[8];
+            block_weights(P, gate, L.column(j, 0), w);
+            add_block(v[j], w, fy, q);
+        } else {
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] = q[i];
+        }
+    }
+    if (P.r_out) store_row<G, RT>(P.r_out, at, L, P.D, v);
+    if (P.x) {
+        const float fx = rsqrtf(block_sum(square_sum<G>(v), part[1], warps) / static_cast<float>(P.D) + P.eps);
+        #pragma unroll
+        for (int j = 0; j < G; ++j) {
+            float w[8];
+            const int k = L.column(j, 0);
+            if (P.pre) load_weights(P.pre + k, k < P.D, k + 128 < P.D, w);
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) v[j][i] = P.pre ? v[j][i] * fx * w[i] : v[j][i] * fx;
+        }
+        store_x<G>(P, row, L, lane, v);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+template <class F>
+cudaError_t by_types(const q4_0_block &b, F &&f) {
     using B = __nv_bfloat16;
-    return yf ? rf ? launch_dependent(block_norm_kernel<G, T, float, float>, grid, threads, s, p)
-                   : launch_dependent(block_norm_kernel<G, T, float, B>, grid, threads, s, p)
-              : rf ? launch_dependent(block_norm_kernel<G, T, B, float>, grid, threads, s, p)
-                   : launch_dependent(block_norm_kernel<G, T, B, B>, grid, threads, s, p);
+    const bool yf = !b.y || b.y_type == Q4_TYPE_F32, rf = b.r_type == Q4_TYPE_F32;
+    if (yf) return rf ? f(float(), float()) : f(float(), B());
+    return rf ? f(B(), float()) : f(B(), B());
+}
+
+template <int G, int T, bool EAGER>
+cudaError_t launch_rows(const q4_0_block &b, const NormParams &p, int warps, cudaStream_t s) {
+    return by_types(b, [&](auto y, auto r) {
+        return launch_dependent(block_norm_kernel<G, T, EAGER, decltype(y), decltype(r)>, p.M, 32 * warps, s, p);
+    });
+}
+
+template <int G>
+cudaError_t launch_many(const q4_0_block &b, const NormParams &p, int warps, const q4::DeviceInfo &dev, cudaStream_t s) {
+    return by_types(b, [&](auto y, auto r) {
+        const auto kernel = block_norm_many_kernel<G, decltype(y), decltype(r)>;
+        constexpr int most = kManyThreads * G * 8 * (sizeof(y) + sizeof(r));
+        if (most > 47 * 1024) {   // more than a CTA gets unasked, with the sums beside it
+            static q4::DeviceOnce configured;
+            const cudaError_t e = configured.run(dev.device, [&] {
+                return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+            });
+            if (e != cudaSuccess) return e;
+        }
+        const size_t bytes = static_cast<size_t>(32 * warps) * G * 8 * ((p.y ? sizeof(y) : 0) + sizeof(r));
+        return launch_dependent_smem(kernel, p.M, 32 * warps, bytes, s, p);
+    });
 }
 
 }  // namespace
@@ -188,25 +408,24 @@ cudaError_t launch_block_norm(const q4_0_block &b, const DeviceInfo &dev, cudaSt
     p.gate = b.gate;
     p.pre = b.pre_weight;
     p.M = b.M;
-    p.D = b.D;
     p.gate_span = b.gate_span;
-    p.kt = mx_k_tiles(b.D);
+    p.D = static_cast<int>(b.D);
+    p.kt = static_cast<int>(mx_k_tiles(b.D));
     p.scale = b.scale;
     p.eps = b.eps;
-    p.y_type = b.y ? b.y_type : Q4_TYPE_F32;
-    p.r_type = b.r_type;
     p.x_type = b.x_type;
-    // few rows: as many threads as the row has groups, for the shortest time
-    // of a row; many: two or four groups a thread, so that a CTA's sums hold
-    // up fewer warps and several CTAs fit on an SM
-    const int64_t groups = b.D / 8;
-    const bool few = b.M <= dev.sm_count;
-    const int G = groups <= (few ? 1024 : 256) ? 1 : groups <= (few ? 2048 : 1024) ? 2 : 4;
-    const int threads = static_cast<int>(((groups + G - 1) / G + 31) / 32 * 32);
-    const int64_t cap = static_cast<int64_t>(dev.sm_count) * 64, grid = b.M < cap ? b.M : cap;
-    if (G == 1) return launch<1, 1024>(p, threads, grid, s);
-    if (threads <= 512) return G == 2 ? launch<2, 512>(p, threads, grid, s) : launch<4, 512>(p, threads, grid, s);
-    return G == 2 ? launch<2, 1024>(p, threads, grid, s) : launch<4, 1024>(p, threads, grid, s);
+    const int groups = p.kt;   // of a warp: 256 values
+    // MANY RULE
+    if (b.M > dev.sm_count && groups <= 32) {
+        if (groups <= 4) return launch_many<1>(b, p, groups, dev, s);
+        if (groups <= 8) return launch_many<2>(b, p, (groups + 1) / 2, dev, s);
+        return launch_many<4>(b, p, (groups + 3) / 4, dev, s);
+    }
+    // as many warps as the row has groups, for the shortest time of a row
+    if (groups <= 16) return launch_rows<1, 512, true>(b, p, groups, s);
+    if (groups <= 32) return launch_rows<1, 1024, true>(b, p, groups, s);
+    if (groups <= 64) return launch_rows<2, 1024, true>(b, p, (groups + 1) / 2, s);
+    return launch_rows<4, 1024, false>(b, p, (groups + 3) / 4, s);
 }
 
 }  // namespace q4
