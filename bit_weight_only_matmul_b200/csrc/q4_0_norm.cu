@@ -106,12 +106,12 @@ struct Lane {
 
 template <int G>
 __device__ __forceinline__ float square_sum(const float (&v)[G][8]) {
-    float ss = 0.f;
+    float ss[4] = {};   // four chains: one would wait for itself at every step
     #pragma unroll
     for (int j = 0; j < G; ++j)
         #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
-    return ss;
+        for (int i = 0; i < 8; ++i) ss[i & 3] = fmaf(v[j][i], v[j][i], ss[i & 3]);
+    return (ss[0] + ss[1]) + (ss[2] + ss[3]);
 }
 
 // w = post * gate of a group (1 where one is missing).
