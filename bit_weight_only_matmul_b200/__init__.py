@@ -1,12 +1,13 @@
 """Python binding of libq4_0_b200.so, the B200 (sm_100a) Q4_0 dequant-matmul
 library (C ABI in include/q4_0.h).
 
-Argument marshalling only: every function takes torch CUDA tensors (or raw
-device addresses), passes their pointers, sizes and the current CUDA stream to
-the C entry point of the same name, and raises ``Q4Error`` on a non-zero
-status.  All arithmetic runs in the library's CUDA kernels; there is no CPU
+Argument marshalling only: every function takes torch CUDA tensors (the Q4_0
+functions also raw device addresses), passes their pointers, sizes and the
+current CUDA stream to the C entry point of the same name, and raises
+``Q4Error`` on a non-zero status.  All arithmetic runs in the library's CUDA kernels; there is no CPU
 path.  Importing this package fails loudly if the library has not been built
-(``python bit_weight_only_matmul_b200/build.py``).
+(``python bit_weight_only_matmul_b200/build.py``), the extension module with
+its checks among it.
 """
 from __future__ import annotations
 
@@ -138,6 +139,12 @@ def _load() -> ctypes.CDLL:
 
 _lib = _load()
 lib = _lib
+
+if not os.path.exists(os.path.join(_HERE, "_binding.so")):
+    raise ImportError(f"{_HERE}/_binding.so is missing: build it with `python bit_weight_only_matmul_b200/build.py`")
+import torch  # noqa: E402, F401  (its libraries, which the extension module is linked to)
+
+from . import _binding  # noqa: E402
 
 
 def _ptr(t) -> Optional[int]:
@@ -284,90 +291,46 @@ def q4_0_quantize(X, W, N: int, K: int, stream=None) -> None:
     _check(_lib.q4_0_quantize(_ptr(X), _ptr(W), N, K, _stream(stream)), "q4_0_quantize")
 
 
-_types: dict = {}
-
-
-def _type(t) -> int:
-    """The Q4_TYPE_* of a tensor's dtype, -1 for none."""
-    if not _types:
-        import torch
-        _types.update({torch.float32: Q4_TYPE_F32, torch.bfloat16: Q4_TYPE_BF16, torch.float16: Q4_TYPE_F16,
-                       torch.uint8: Q4_TYPE_MXFP4})
-    return _types.get(t.dtype, -1)
-
-
-def _device(t, what: str) -> int:
-    """The current device, which `t` must be on."""
-    d = t.get_device()
-    if d < 0:
-        raise ValueError(f"{what}: expected a CUDA tensor")
-    import torch
-    if d != torch.cuda.current_device():
-        raise ValueError(f"{what}: on device {d}, the current device is {torch.cuda.current_device()}")
-    return d
-
-
-def _operand(t, what: str, types: Sequence[int], count: int, device: int) -> int:
-    """Device address of a tensor that must be contiguous, on `device`, of one
-    of `types` and hold at least `count` elements."""
-    if (t.get_device() == device and _types.get(t.dtype, -1) in types and t.is_contiguous() and t.numel() >= count):
-        return t.data_ptr()
-    _device(t, what)
-    if _type(t) not in types:
-        raise ValueError(f"{what}: dtype {t.dtype} is not supported here")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous tensor")
-    if t.numel() < count:
-        raise ValueError(f"{what}: {t.numel()} elements, {count} are needed")
-    return t.data_ptr()
-
-
-_VALUES = (Q4_TYPE_F32, Q4_TYPE_BF16, Q4_TYPE_F16)
-_F32, _F32_BF16, _BYTES = (Q4_TYPE_F32,), (Q4_TYPE_F32, Q4_TYPE_BF16), (Q4_TYPE_MXFP4,)
-
-
 def mxfp4_bytes(R: int, K: int) -> int:
     """Bytes of an MXFP4 matrix of R rows by K values (include/mxfp4.h), -1
     for sizes it cannot have."""
     return int(_lib.mxfp4_bytes(R, K))
 
 
-def _mx(t, what: str, R: int, K: int, device: int) -> int:
-    """Device address of an MXFP4 matrix (sizes it cannot have are refused by the library)."""
-    return _operand(t, what, _BYTES, (R + 127) // 128 * ((K + 255) // 256) * 17408, device)
-
+# The functions below raise ValueError for a tensor that is not contiguous, not
+# on the current device, too small or of a type the operator does not take
+# (csrc/binding.cpp), and Q4Error for what the library refuses.
 
 def mxfp4_quantize(X, W, R: int, K: int, stream=None) -> None:
     """X [R, K] (float32, bfloat16 or float16) to the MXFP4 matrix W (uint8,
     mxfp4_bytes(R, K))."""
-    d = _device(X, "X")
-    _check(_lib.mxfp4_quantize(_operand(X, "X", _VALUES, R * K, d), _type(X), _mx(W, "W", R, K, d), R, K, _stream(stream)),
-           "mxfp4_quantize")
+    status = _binding.mxfp4_quantize(X, W, R, K, stream)
+    if status != Q4_OK:
+        raise Q4Error(status, "mxfp4_quantize")
 
 
 def mxfp4_dequant(W, out, R: int, K: int, stream=None) -> None:
     """The values of the MXFP4 matrix W: out [R, K] float32, bfloat16 (both
     exact) or float16."""
-    d = _device(W, "W")
-    _check(_lib.mxfp4_dequant(_mx(W, "W", R, K, d), _operand(out, "out", _VALUES, R * K, d), _type(out), R, K,
-                              _stream(stream)), "mxfp4_dequant")
+    status = _binding.mxfp4_dequant(W, out, R, K, stream)
+    if status != Q4_OK:
+        raise Q4Error(status, "mxfp4_dequant")
 
 
 def mxfp4_pack(codes, scales, W, R: int, K: int, stream=None) -> None:
     """codes uint8 [R, K/2] (two to a byte, the lower k in the low bits) and
     scales uint8 [R, K/32] (E + 127) -> the MXFP4 matrix W."""
-    d = _device(codes, "codes")
-    _check(_lib.mxfp4_pack(_operand(codes, "codes", _BYTES, R * (K // 2), d),
-                           _operand(scales, "scales", _BYTES, R * (K // 32), d), _mx(W, "W", R, K, d), R, K,
-                           _stream(stream)), "mxfp4_pack")
+    status = _binding.mxfp4_pack(codes, scales, W, R, K, stream)
+    if status != Q4_OK:
+        raise Q4Error(status, "mxfp4_pack")
 
 
 def mxfp4_gemm(W, X, Y, M: int, N: int, K: int, stream=None) -> None:
     """Y[M,N] = X[M,K] * W[N,K]^T, W and X MXFP4 matrices (uint8), Y float32
     or bfloat16."""
-    d = _device(W, "W")
-    _check(_lib.mxfp4_gemm(_mx(W, "W", N, K, d), _mx(X, "X", M, K, d), _operand(Y, "Y", _F32_BF16, M * N, d), _type(Y),
-                           M, N, K, _stream(stream)), "mxfp4_gemm")
+    status = _binding.mxfp4_gemm(W, X, Y, M, N, K, stream)
+    if status != Q4_OK:
+        raise Q4Error(status, "mxfp4_gemm")
 
 
 def q4_0_block_norm(r, M: int, D: int, y=None, post_weight=None, gate=None, gate_span: int = 0, scale: float = 1.0,
@@ -376,27 +339,9 @@ def q4_0_block_norm(r, M: int, D: int, y=None, post_weight=None, gate=None, gate
     r_out = r + scale * gate * norm(y, post_weight) and x = norm(r_out,
     pre_weight), x float32, bfloat16 or an MXFP4 matrix (uint8).  See
     include/q4_0.h for what may be left out."""
-    d = _device(r, "r")
-    n = M * D
-    r_type = _type(r)
-    yp = op = xp = postp = gatep = prep = None
-    y_type = x_type = 0
-    if y is not None:
-        yp, y_type = _operand(y, "y", _F32_BF16, n, d), _type(y)
-    if r_out is not None:
-        op = _operand(r_out, "r_out", (r_type,), n, d)
-    if x is not None:
-        x_type = _type(x)
-        xp = _mx(x, "x", M, D, d) if x_type == Q4_TYPE_MXFP4 else _operand(x, "x", _F32_BF16, n, d)
-    if post_weight is not None:
-        postp = _operand(post_weight, "post_weight", _F32, D, d)
-    if gate is not None:
-        gatep = _operand(gate, "gate", _F32, D * (-(-M // gate_span) if gate_span > 0 else 1), d)
-    if pre_weight is not None:
-        prep = _operand(pre_weight, "pre_weight", _F32, D, d)
-    b = q4_0_block(yp, _operand(r, "r", _F32_BF16, n, d), op, xp, postp, gatep, prep, M, D, gate_span, scale, eps, y_type,
-                   r_type, x_type)
-    _check(_lib.q4_0_block_norm(ctypes.byref(b), _stream(stream)), "q4_0_block_norm")
+    status = _binding.q4_0_block_norm(r, M, D, y, post_weight, gate, gate_span, scale, pre_weight, x, r_out, eps, stream)
+    if status != Q4_OK:
+        raise Q4Error(status, "q4_0_block_norm")
 
 
 def q4_0_device_error(clear: bool = True) -> int:

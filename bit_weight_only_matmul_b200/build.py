@@ -10,15 +10,21 @@ bit_weight_only_matmul_b200/libq4_0_b200.so.  --debug builds the same sources
 with Q4_DEBUG defined (index checks in the decode and tensor-core kernels that
 report Q4_DEVERR_DEBUG_CHECK instead of touching memory outside a buffer)
 into _build_debug/ and libq4_0_b200_debug.so.
+
+csrc/binding.cpp, the binding's checks as a CPython extension module, is
+compiled with the host compiler against the headers of the interpreter and
+the torch it runs with, and linked to the library beside it (_binding.so).
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,6 +34,7 @@ LIB = os.path.join(PKG, "libq4_0_b200.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libq4_0_b200_debug.so")
 INCLUDE = os.path.join(ROOT, "include")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -80,6 +87,26 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
     return lib
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The extension module, after the library that it is linked to."""
+    src = os.path.join(CSRC, "binding.cpp")
+    newest = max(os.path.getmtime(f) for f in (src, *glob.glob(os.path.join(INCLUDE, "*.h"))))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-I{sysconfig.get_paths()['include']}", "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"), f"-I{INCLUDE}", src, "-o", tmp,
+           f"-L{PKG}", f"-l:{os.path.basename(LIB)}", f"-L{os.path.join(torch, 'lib')}", "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-Wl,-rpath,$ORIGIN"]   # torch's own are loaded already when the module is
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser()
     ap.add_argument("--force", action="store_true")
@@ -88,6 +115,8 @@ def main(argv=None) -> int:
     ap.add_argument("--debug", action="store_true", help="build libq4_0_b200_debug.so with Q4_DEBUG index checks")
     a = ap.parse_args(argv)
     print(build(a.force, a.verbose, a.ptxas_info, a.debug))
+    if not a.debug:
+        print(build_binding(a.force, a.verbose))
     return 0
 
 
