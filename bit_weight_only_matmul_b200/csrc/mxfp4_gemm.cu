@@ -8,9 +8,9 @@
 // one row of Y and a store is one contiguous run, and a few activation rows
 // cost an MMA of few columns.  Both kernels have
 //   * producer warps that bring the tiles of a 256-k step with bulk copies. A
-//     warp issues one copy in about 100 cycles plus one for each 77 bytes, so
-//     each of the step's larger copies has a warp of its own (one warp for all
-//     of them: 1.5 times the time of a whole prompt);
+//     warp issues one copy in about 100 cycles plus one for each 77 bytes (one
+//     warp 52 bytes a cycle in copies of 16 KB, two 68), so each of the step's
+//     larger copies has a warp of its own;
 //   * a warp that copies the step's scales from shared to tensor memory (each
 //     ring slot has its own columns there) and issues four MMAs of K = 64.
 //     The whole warp walks the loop and one elected lane issues, so that the
@@ -49,8 +49,8 @@ __device__ __forceinline__ bool try_phase(uint64_t *bar, uint32_t parity) {
 }
 
 // Bounded wait that also gives up when another role has aborted.  The global
-// timer is read only once a wait has failed often enough to be out of the
-// ordinary: reading it takes longer than a step of the product.
+// timer is read, and the error word at hand, only once a wait has failed often
+// enough to be out of the ordinary.
 template <bool CLUSTER>
 __device__ __noinline__ bool long_wait(uint64_t *bar, uint32_t parity, int *abort_flag, unsigned *err) {
     const unsigned long long t0 = global_ns();
@@ -175,13 +175,12 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
     __syncthreads();
     if (P.split > 1) cluster_sync_all();   // every CTA's barrier exists before another CTA arrives on it
     tc_fence_after();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_dependent();   // all warps: their waits are bounded, the kernel before is not
     const uint32_t tmem = S.tmem_base;
 
     if (warp == 0) {
         // the weight tiles
         if (lane == 0) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
             const uint8_t *w = P.W + (static_cast<int64_t>(tn) * P.kt + k0) * kMxTileBytes;
             int c = 0;
             for (; c < k1 - k0; ++c, w += kMxTileBytes) {
@@ -195,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
     } else if (warp == 6) {
         // the activation rows and their scales
         if (lane == 0) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
             const uint8_t *x = P.X + static_cast<int64_t>(k0) * kMxTileBytes;
             int c = 0;
             for (; c < k1 - k0; ++c, x += kMxTileBytes) {
@@ -438,7 +436,6 @@ __device__ __forceinline__ TilePlace place_of(const PairParams &P, int t) {
 template <int SLOTS, class Copy>
 __device__ __forceinline__ void produce(const PairParams &P, PairSmem &S, int first, int step, int rank, int bytes, Copy &&copy) {
     if ((threadIdx.x & 31) != 0) return;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     int s = 0, issued = 0;
     uint32_t parity = 1;
     for (int t = first; t < P.tiles; t += step) {
@@ -481,7 +478,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
     __syncthreads();
     cluster_sync_all();   // the other CTA's barriers exist
     tc_fence_after();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_dependent();   // all warps: their waits are bounded, the kernel before is not
     const uint32_t tmem = S.tmem_base;
 
     if (warp == 0) {
@@ -500,10 +497,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
                 tma_load_pair(smem_addr(ring) + s * C::kSlotBytes + kMxTileBytes + C::kXCodes + 1024 * h, &P.map_xs,
                               17 * (min(XN / 128 * at.m + h, P.xt - 1) * P.kt + i) + 16, bar);
         });
-    } else if (warp == 1 && rank == 1) {
-        // the first CTA's last commit arrives here too, before this CTA may leave
-        wait_or_abort(&S.mma_done, 0, &S.abort_flag, P.err) || mbar_wait(&S.mma_done, 0, P.err);
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
         constexpr uint32_t idesc = mxf4_idesc(256, XN, 0);
         int s = 0;
         uint32_t parity = 0, dpar = 1;
@@ -538,10 +532,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
             }
         }
         // every MMA issued so far has completed once this commit arrives
-        if (elect_one()) tc_commit_pair(&S.mma_done);
+        if (elect_one()) tc_commit_pair_own(&S.mma_done);
         __syncwarp();
         wait_or_abort(&S.mma_done, 0, &S.abort_flag, P.err) || mbar_wait(&S.mma_done, 0, P.err);
-    } else {
+    } else if (warp >= 2) {
         const int quad = warp & 3, half = (warp - 2) >> 2;   // lanes [32 quad, +32), columns [XN/2 half, +XN/2)
         uint32_t parity = 0;
         for (int t = first; t < P.tiles; t += step, parity ^= 1) {

@@ -65,6 +65,12 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
         : "memory");
 }
 
+// Arrives on the issuing CTA's barrier only.
+__device__ __forceinline__ void tc_commit_pair_own(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
 // TMA load of a box of whole 1 KB rows from row y on, into this CTA's shared
 // memory; `bar` is a shared::cluster address and may lie in the pair's other CTA.
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *map, int y, uint32_t bar) {

@@ -20,7 +20,9 @@
 // block_norm_many_kernel lands them in shared memory first (each thread copies
 // what it will read itself, so nobody waits for anybody), which leaves room on
 // an SM for twice as many rows: a row's time is mostly waiting, for memory and
-// for its two sums.
+// for its two sums.  Keeping all values in registers, 4096 x 8192 fp32 took
+// 97 us against 77 (6.1 TB/s); a persistent kernel with a ring of rows in shared
+// memory 80, and more than this one for shorter rows (4096 x 5120 80 against 55).
 #include "mxfp4_layout.cuh"
 
 namespace {
@@ -156,33 +158,39 @@ __device__ __forceinline__ void store_row(void *p, int64_t at, const Lane<G> &L,
 // warps take part (blocks past D: zero codes and a zero scale byte).
 template <int G>
 __device__ __forceinline__ void store_mxfp4(const NormParams &P, int64_t row, const Lane<G> &L, int lane, const float (&v)[G][8]) {
+    uint32_t a[G][2];   // the blocks' largest magnitudes, all on their way at once
+    #pragma unroll
+    for (int j = 0; j < G; ++j)
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            a[j][h] = 0;
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) a[j][h] = max(a[j][h], __float_as_uint(v[j][4 * h + i]) & 0x7FFFFFFFu);
+        }
+    #pragma unroll
+    for (int o = 1; o < 8; o <<= 1)
+        #pragma unroll
+        for (int j = 0; j < G; ++j)
+            #pragma unroll
+            for (int h = 0; h < 2; ++h) a[j][h] = max(a[j][h], __shfl_xor_sync(0xffffffffu, a[j][h], o));
     const int r = static_cast<int>(row & 127);
+    uint8_t *const tiles = static_cast<uint8_t *>(P.x) + (row >> 7) * P.kt * q4::kMxTileBytes;
     #pragma unroll
     for (int j = 0; j < G; ++j) {
         const int k = L.column(j, 0), tile_k = k >> 8;   // the same in the whole warp
-        if (tile_k >= P.kt) break;
-        uint8_t *tile = static_cast<uint8_t *>(P.x) + ((row >> 7) * P.kt + tile_k) * q4::kMxTileBytes;
-        #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const bool live = k + 128 * h < P.D;
-            uint32_t a = 0;
+        if (tile_k < P.kt) {
+            uint8_t *tile = tiles + static_cast<int64_t>(tile_k) * q4::kMxTileBytes;
             #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t b = __float_as_uint(v[j][4 * h + i]) & 0x7FFFFFFFu;
-                a = a > b ? a : b;
+            for (int h = 0; h < 2; ++h) {
+                const bool live = k + 128 * h < P.D;
+                const uint32_t byte = live ? mx_scale_byte(a[j][h]) : 0u;
+                const float inv = mx_inverse_scale(byte);
+                const float *u = v[j] + 4 * h;
+                const uint32_t code = live ? e2m1x4(u[0] * inv, u[1] * inv, u[2] * inv, u[3] * inv) : 0u;
+                const int b = 4 * h + (lane >> 3);
+                *reinterpret_cast<uint16_t *>(tile + mx_code_offset(r, b) + 2 * (lane & 7)) = static_cast<uint16_t>(code);
+                if ((lane & 7) == 0) tile[mx_scale_offset(r, h) + (lane >> 3)] = static_cast<uint8_t>(byte);
             }
-            #pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                const uint32_t b = __shfl_xor_sync(0xffffffffu, a, o);
-                a = a > b ? a : b;
-            }
-            const uint32_t byte = live ? mx_scale_byte(a) : 0u;
-            const float inv = mx_inverse_scale(byte);
-            const float *u = v[j] + 4 * h;
-            const uint32_t code = live ? e2m1x4(u[0] * inv, u[1] * inv, u[2] * inv, u[3] * inv) : 0u;
-            const int b = 4 * h + (lane >> 3);
-            *reinterpret_cast<uint16_t *>(tile + mx_code_offset(r, b) + 2 * (lane & 7)) = static_cast<uint16_t>(code);
-            if ((lane & 7) == 0) tile[mx_scale_offset(r, h) + (lane >> 3)] = static_cast<uint8_t>(byte);
         }
     }
 }
@@ -308,10 +316,12 @@ struct Landing {
     }
 };
 
-constexpr int kManyThreads = 256;
+// Threads at most, and CTAs an SM that the registers must leave room for.
+constexpr int many_threads(int G) { return G == 4 ? 256 : 512; }
+constexpr int many_ctas(int G) { return G == 4 ? 3 : 1; }
 
 template <int G, class YT, class RT>
-__global__ void __launch_bounds__(kManyThreads, 3) block_norm_many_kernel(const __grid_constant__ NormParams P) {
+__global__ void __launch_bounds__(many_threads(G), many_ctas(G)) block_norm_many_kernel(const __grid_constant__ NormParams P) {
     extern __shared__ __align__(16) uint8_t landing[];
     __shared__ float part[2][32];
     begin_dependent();
@@ -381,7 +391,7 @@ template <int G>
 cudaError_t launch_many(const q4_0_block &b, const NormParams &p, int warps, const q4::DeviceInfo &dev, cudaStream_t s) {
     return by_types(b, [&](auto y, auto r) {
         const auto kernel = block_norm_many_kernel<G, decltype(y), decltype(r)>;
-        constexpr int most = kManyThreads * G * 8 * (sizeof(y) + sizeof(r));
+        constexpr int most = many_threads(G) * G * 8 * (sizeof(y) + sizeof(r));
         if (most > 47 * 1024) {   // more than a CTA gets unasked, with the sums beside it
             static q4::DeviceOnce configured;
             const cudaError_t e = configured.run(dev.device, [&] {
@@ -415,10 +425,14 @@ cudaError_t launch_block_norm(const q4_0_block &b, const DeviceInfo &dev, cudaSt
     p.eps = b.eps;
     p.x_type = b.x_type;
     const int groups = p.kt;   // of a warp: 256 values
-    // MANY RULE
+    // More rows than SMs: few warps a row, so that many rows are in flight.
+    // Four groups a thread for long rows, where two would take so many warps a
+    // row that fewer rows fit on an SM (us, four and two: 4096 x 8192 76.6 and
+    // 97.0, 4096 x 5120 bf16 37.5 and 44.6); two for shorter ones (1500 x 4096
+    // 17.2 and 16.0, 4096 x 4096 41.8 and 38.3).
     if (b.M > dev.sm_count && groups <= 32) {
         if (groups <= 4) return launch_many<1>(b, p, groups, dev, s);
-        if (groups <= 8) return launch_many<2>(b, p, (groups + 1) / 2, dev, s);
+        if (groups <= 16) return launch_many<2>(b, p, (groups + 1) / 2, dev, s);
         return launch_many<4>(b, p, (groups + 3) / 4, dev, s);
     }
     // as many warps as the row has groups, for the shortest time of a row
