@@ -92,18 +92,22 @@ __device__ __forceinline__ uint32_t e2m1x4(float a, float b, float c, float d) {
     return r;
 }
 
+// The largest of three magnitudes; NaN if one is NaN.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// The bits of a magnitude, NaN among them above all numbers.
+__device__ __forceinline__ uint32_t magnitude_bits(float a) { return __float_as_uint(a) & 0x7FFFFFFFu; }
+
 // Four consecutive lanes hold a block, eight values each (lane & 3 the part):
 // the lane's code word; `byte` is the block's scale byte in all four lanes.
 // All 32 lanes of the warp take part.  Multiplying by a power of two is exact
 // (what underflows is far below the smallest code's half), so the only
 // rounding is the one to E2M1.
 __device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8], uint32_t &byte) {
-    uint32_t a = 0;
-    #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-        a = a > b ? a : b;
-    }
+    uint32_t a = magnitude_bits(max_abs(max_abs(v[0], v[1], v[2]), max_abs(v[3], v[4], v[5]), max_abs(v[6], v[7], v[7])));
     uint32_t o = __shfl_xor_sync(0xffffffffu, a, 1);
     a = a > o ? a : o;
     o = __shfl_xor_sync(0xffffffffu, a, 2);

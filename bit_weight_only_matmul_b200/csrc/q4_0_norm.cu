@@ -163,9 +163,8 @@ __device__ __forceinline__ void store_mxfp4(const NormParams &P, int64_t row, co
     for (int j = 0; j < G; ++j)
         #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            a[j][h] = 0;
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) a[j][h] = max(a[j][h], __float_as_uint(v[j][4 * h + i]) & 0x7FFFFFFFu);
+            const float *u = v[j] + 4 * h;
+            a[j][h] = magnitude_bits(max_abs(max_abs(u[0], u[1], u[2]), u[3], u[3]));
         }
     #pragma unroll
     for (int o = 1; o < 8; o <<= 1)
