@@ -415,11 +415,10 @@ __device__ __forceinline__ void put(__nv_bfloat16 *y, float v) { *y = __float2bf
 
 // Tile t's place: bands of up to kBand tiles along M, within a band M fastest,
 // so that the tiles worked at one time form a near square and share their
-// weight and activation tiles in L2.
-#ifndef KBAND
-#define KBAND 8
-#endif
-constexpr int kBand = KBAND;
+// weight and activation tiles in L2 (4096 x 16384 x 5120, us: bands of 4 131,
+// of 8 129, of 16 125; one band of all tiles along N first 213 against 200 when
+// it was tried).
+constexpr int kBand = 16;
 struct TilePlace {
     int n, m;
 };

@@ -315,12 +315,11 @@ struct Landing {
     }
 };
 
-// Threads at most, and CTAs an SM that the registers must leave room for.
-constexpr int many_threads(int G) { return G == 4 ? 256 : 512; }
-constexpr int many_ctas(int G) { return G == 4 ? 3 : 1; }
+// CTAs that an SM's registers must leave room for, by groups and threads.
+constexpr int many_ctas(int G, int T) { return T == 256 ? 3 : G == 4 ? 1 : 2; }
 
-template <int G, class YT, class RT>
-__global__ void __launch_bounds__(many_threads(G), many_ctas(G)) block_norm_many_kernel(const __grid_constant__ NormParams P) {
+template <int G, int T, class YT, class RT>
+__global__ void __launch_bounds__(T, many_ctas(G, T)) block_norm_many_kernel(const __grid_constant__ NormParams P) {
     extern __shared__ __align__(16) uint8_t landing[];
     __shared__ float part[2][32];
     begin_dependent();
@@ -386,11 +385,11 @@ cudaError_t launch_rows(const q4_0_block &b, const NormParams &p, int warps, cud
     });
 }
 
-template <int G>
+template <int G, int T>
 cudaError_t launch_many(const q4_0_block &b, const NormParams &p, int warps, const q4::DeviceInfo &dev, cudaStream_t s) {
     return by_types(b, [&](auto y, auto r) {
-        const auto kernel = block_norm_many_kernel<G, decltype(y), decltype(r)>;
-        constexpr int most = many_threads(G) * G * 8 * (sizeof(y) + sizeof(r));
+        const auto kernel = block_norm_many_kernel<G, T, decltype(y), decltype(r)>;
+        constexpr int most = T * G * 8 * (sizeof(y) + sizeof(r));
         if (most > 47 * 1024) {   // more than a CTA gets unasked, with the sums beside it
             static q4::DeviceOnce configured;
             const cudaError_t e = configured.run(dev.device, [&] {
@@ -424,15 +423,15 @@ cudaError_t launch_block_norm(const q4_0_block &b, const DeviceInfo &dev, cudaSt
     p.eps = b.eps;
     p.x_type = b.x_type;
     const int groups = p.kt;   // of a warp: 256 values
-    // More rows than SMs: few warps a row, so that many rows are in flight.
-    // Four groups a thread for long rows, where two would take so many warps a
-    // row that fewer rows fit on an SM (us, four and two: 4096 x 8192 76.6 and
-    // 97.0, 4096 x 5120 bf16 37.5 and 44.6); two for shorter ones (1500 x 4096
-    // 17.2 and 16.0, 4096 x 4096 41.8 and 38.3).
-    if (b.M > dev.sm_count && groups <= 32) {
-        if (groups <= 4) return launch_many<1>(b, p, groups, dev, s);
-        if (groups <= 16) return launch_many<2>(b, p, (groups + 1) / 2, dev, s);
-        return launch_many<4>(b, p, (groups + 3) / 4, dev, s);
+    // More rows than SMs: fewer warps a row, so that more rows are in flight.
+    // Two groups a thread, four for the longest rows (us, two and four: 1001 x
+    // 4128 bf16 10.2 and 11.6, 4096 x 5120 46.9 and 50.9, 4096 x 6144 bf16 and
+    // fp32 49.0 and 51.8; 4096 x 8192 74.0 and 75.8, in bf16 59.4 and 55.4).
+    if (b.M > dev.sm_count && groups <= 64) {
+        if (groups <= 4) return launch_many<1, 512>(b, p, groups, dev, s);
+        if (groups <= 24) return launch_many<2, 512>(b, p, (groups + 1) / 2, dev, s);
+        if (groups <= 32) return launch_many<4, 256>(b, p, (groups + 3) / 4, dev, s);
+        return launch_many<4, 512>(b, p, (groups + 3) / 4, dev, s);
     }
     // as many warps as the row has groups, for the shortest time of a row
     if (groups <= 16) return launch_rows<1, 512, true>(b, p, groups, s);
