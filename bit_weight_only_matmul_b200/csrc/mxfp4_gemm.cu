@@ -136,10 +136,22 @@ __device__ __forceinline__ uint32_t remote_addr(uint32_t local, uint32_t rank) {
     return ra;
 }
 
-__device__ __forceinline__ void store_y(const SplitParams &P, int m, int64_t n, float v) {
-    const int64_t at = m * P.N + n;
-    if (P.bf16) static_cast<__nv_bfloat16 *>(P.Y)[at] = __float2bfloat16_rn(v);
-    else static_cast<float *>(P.Y)[at] = v;
+__device__ __forceinline__ void put(float *y, float v) { *y = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *y, float v) { *y = __float2bfloat16_rn(v); }
+
+// A warp's 32 lanes of the accumulator to column n of Y's rows.
+template <class T>
+__device__ __forceinline__ void store_columns(const SplitParams &P, uint32_t d, int64_t n) {
+    T *y = static_cast<T *>(P.Y) + n;
+    #pragma unroll 1
+    for (int c = 0; c < P.M; c += 8) {
+        float v[8];
+        tc_ld_cols<8>(d + c, v);
+        tc_wait_ld();
+        #pragma unroll
+        for (int j = 0; j < 8; ++j, y += P.N)
+            if (n < P.N && c + j < P.M) put(y, v[j]);
+    }
 }
 
 __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_constant__ SplitParams P) {
@@ -165,10 +177,12 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
         mbar_init(&S.red_full, 4 * P.split);
         S.abort_flag = 0;
         fence_mbar_init();
+    }
+    if (warp >= 2 && lane == 0) {
         // the first weight tiles on their way to L2 while the kernel before
         // this one ends
         const uint8_t *w = P.W + (static_cast<int64_t>(tn) * P.kt + k0) * kMxTileBytes;
-        for (int i = 0; i < P.slots && k0 + i < k1; ++i) bulk_prefetch_l2(w + static_cast<int64_t>(i) * kMxTileBytes, kMxTileBytes);
+        for (int i = warp - 2; i < P.slots && k0 + i < k1; i += 5) bulk_prefetch_l2(w + static_cast<int64_t>(i) * kMxTileBytes, kMxTileBytes);
     }
     if (warp == 1) tmem_alloc(&S.tmem_base, kSplitTmemCols);
     tc_fence_before();
@@ -246,17 +260,8 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
     if (warp >= 2 && warp < 6 && all_lanes(wait_or_abort(&S.d_full, 0, &S.abort_flag, P.err))) {
         tc_fence_after();
         if (P.split == 1) {
-            #pragma unroll 1
-            for (int c = 0; c < live; c += 8) {
-                float v[8];
-                tc_ld_cols<8>(d + c, v);
-                tc_wait_ld();
-                if (n < P.N) {
-                    #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (c + j < live) store_y(P, c + j, n, v[j]);
-                }
-            }
+            if (P.bf16) store_columns<__nv_bfloat16>(P, d, n);
+            else store_columns<float>(P, d, n);
         } else {
             const int cpr = (P.xcap + P.split - 1) / P.split;   // columns a rank adds
             const uint32_t mine = smem_addr(red + rank * cpr * 128 + row);
@@ -286,7 +291,8 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
                     const float *p = red + (c - rank * cpr) * 128 + row;
                     float v = 0.f;
                     for (int q = 0; q < P.split; ++q) v += p[q * cpr * 128];
-                    store_y(P, c, n, v);
+                    if (P.bf16) put(static_cast<__nv_bfloat16 *>(P.Y) + c * P.N + n, v);
+                    else put(static_cast<float *>(P.Y) + c * P.N + n, v);
                 }
             }
         }
@@ -409,9 +415,6 @@ __device__ __forceinline__ void arrive_remote(uint64_t *bar, uint32_t rank) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_addr(smem_addr(bar), rank))
                  : "memory");
 }
-
-__device__ __forceinline__ void put(float *y, float v) { *y = v; }
-__device__ __forceinline__ void put(__nv_bfloat16 *y, float v) { *y = __float2bfloat16_rn(v); }
 
 // Tile t's place: bands of up to kBand tiles along M, within a band M fastest,
 // so that the tiles worked at one time form a near square and share their
