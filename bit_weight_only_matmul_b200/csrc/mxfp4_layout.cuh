@@ -47,17 +47,16 @@ __device__ __forceinline__ int mx_scale_offset(int r, int g) {
     return q4::kMxCodeBytes + 512 * g + 16 * (r & 31) + 4 * (r >> 5);
 }
 
-// The scale byte of a block whose largest magnitude has the bits `amax`
-// (sign bit clear): E + 127 with E = floor(log2 amax) - 2, at least 0; 255
-// (NaN) for a block with an infinity or a NaN.  The exponent field of amax is
-// floor(log2 amax) + 127 (0 for a subnormal, whose E is below the range).
+// Of a block whose largest magnitude has the bits `amax` (sign bit clear): its
+// scale byte, E + 127 with E = floor(log2 amax) - 2, at least 0; 255 (NaN) with
+// an infinity or a NaN.  The exponent field of amax is floor(log2 amax) + 127
+// (0 for a subnormal, whose E is below the range).
 __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax) {
     const uint32_t e = amax >> 23;
-    return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+    return e == 255u ? 255u : max(e, 2u) - 2u;
 }
-
-// 2^-E of a scale byte (for byte 255 any number: the block is NaN anyway).
-__device__ __forceinline__ float mx_inverse_scale(uint32_t byte) { return __uint_as_float((254u - (byte < 253u ? byte : 252u)) << 23); }
+// And 2^-E (for a block that is NaN any number).
+__device__ __forceinline__ float mx_inverse_scale(uint32_t amax) { return __uint_as_float((256u - max(amax >> 23, 2u)) << 23); }
 
 // 2^E of a scale byte; NaN for 255.
 __device__ __forceinline__ float mx_scale(uint32_t byte) {
@@ -108,25 +107,14 @@ __device__ __forceinline__ uint32_t magnitude_bits(float a) { return __float_as_
 // rounding is the one to E2M1.
 __device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8], uint32_t &byte) {
     uint32_t a = magnitude_bits(max_abs(max_abs(v[0], v[1], v[2]), max_abs(v[3], v[4], v[5]), max_abs(v[6], v[7], v[7])));
-    uint32_t o = __shfl_xor_sync(0xffffffffu, a, 1);
-    a = a > o ? a : o;
-    o = __shfl_xor_sync(0xffffffffu, a, 2);
-    a = a > o ? a : o;
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
     byte = mx_scale_byte(a);
-    const float inv = mx_inverse_scale(byte);
+    const float inv = mx_inverse_scale(a);
     float s[8];
     #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] = v[i] * inv;
     return e2m1x8(s);
-}
-
-// The warp's eight scale bytes (one per four lanes) as the word of this
-// lane's half (blocks 4g .. 4g+3 for lanes 16g .. 16g+15).
-__device__ __forceinline__ uint32_t mx_scale_word(uint32_t byte, int lane) {
-    uint32_t w = byte << (8 * ((lane >> 2) & 3));
-    w |= __shfl_xor_sync(0xffffffffu, w, 4);
-    w |= __shfl_xor_sync(0xffffffffu, w, 8);
-    return w;
 }
 
 // Eight values as they lie in memory.

@@ -8,12 +8,14 @@
 // shuffles, and writes each row's 128 bytes of codes as one line and its
 // eight scale bytes from eight lanes.
 //
-// Bound by HBM.  Eight rows a warp keep more in flight where there are warps
-// enough (8192 x 8192 bf16 quantize 35.7 us against 39.9 with two rows, dequant
-// of 16384 x 5120 to bf16 35.1 against 44.2); two spread few rows over the SMs
-// (1003 x 4128 fp16 quantize 4.3 us against 5.9), and are enough for fp32,
-// whose rows are twice as many bytes (16384 x 5120 quantize 57.8 against 59.0 us,
-// dequant 64.0 against 72.5).
+// Bound by HBM (16384 x 5120: quantize of fp32 57.8 us, 6.6 TB/s, dequant to bf16
+// 35.2 us, 6.0 TB/s), and for 16-bit values by the instructions too (quantize of
+// 8192 x 8192 bf16 29.8 us, 5.7 TB/s).  Eight rows a warp keep more in flight
+// where there are warps enough (that quantize 35.7 us against 39.9 with two
+// rows when it was chosen, dequant to bf16 35.1 against 44.2); two spread few
+// rows over the SMs (1003 x 4128 fp16 quantize 4.3 us against 5.9, now 3.7), and
+// are enough for fp32, whose rows are twice as many bytes (16384 x 5120 quantize
+// 57.8 against 59.0 us, dequant 64.0 against 72.5).
 #include "mxfp4_layout.cuh"
 
 namespace {
@@ -23,39 +25,41 @@ using q4::kMxTileBytes;
 
 constexpr int kWarps = 4;       // warps of a CTA
 
-// A warp's part of the matrix, ROWS rows or the last few: rows row0 .. row0 + rows - 1 of tile column t.
+// A warp's part of the matrix, ROWS rows or the last few of one tile column.
+// ROWS divides 8, so that row i of the part is row (r & 7) | i of its group of
+// eight in the swizzle, and r + i stays within 32 rows of scales.
 struct Part {
-    int64_t row0, k;   // k: the lane's first value
-    int rows, r;       // r: row0's place in its tile
-    uint8_t *tile;
+    int64_t at;        // the lane's first value of the first row
+    int rows;
+    uint8_t *codes;    // the first row's codes
+    uint8_t *scales;   // the first row's scales, blocks 0 to 3
+    uint8_t *scale;    // the lane's block's scale byte of the first row
+    int word;          // the lane's code word in a row, swizzled as in the first
     bool live;         // the lane's values lie within K
 };
 
 template <int ROWS>
 __device__ __forceinline__ bool part_of(Part &p, const uint8_t *W, int64_t R, int64_t K, int kt) {
-    const int lane = threadIdx.x & 31;
+    static_assert(8 % ROWS == 0, "a part lies in a group of eight rows");
+    const int lane = threadIdx.x & 31, b = lane >> 2;
     const uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const uint32_t g = u / static_cast<uint32_t>(kt), t = u - g * kt;
-    p.row0 = static_cast<int64_t>(g) * ROWS;
-    if (p.row0 >= R) return false;
-    p.rows = R - p.row0 < ROWS ? static_cast<int>(R - p.row0) : ROWS;
-    p.r = static_cast<int>(p.row0 & 127);
-    p.tile = const_cast<uint8_t *>(W) + ((p.row0 >> 7) * kt + t) * kMxTileBytes;
-    p.k = static_cast<int64_t>(t) * 256 + 8 * lane;
-    p.live = p.k < K;
+    const int64_t row = static_cast<int64_t>(g) * ROWS, k = static_cast<int64_t>(t) * 256 + 8 * lane;
+    if (row >= R) return false;
+    p.rows = R - row < ROWS ? static_cast<int>(R - row) : ROWS;
+    const int r = static_cast<int>(row & 127);
+    uint8_t *tile = const_cast<uint8_t *>(W) + ((row >> 7) * kt + t) * kMxTileBytes;
+    p.codes = tile + 128 * r;
+    p.word = mx_code_offset(r, b) - 128 * r + 4 * (lane & 3);
+    p.scales = tile + mx_scale_offset(r, 0);
+    p.scale = p.scales + 512 * (b >> 2) + (b & 3);
+    p.live = k < K;
+    p.at = row * K + k;
     return true;
 }
 
-__device__ __forceinline__ uint32_t *code_word(const Part &p, int i, int lane) {
-    return reinterpret_cast<uint32_t *>(p.tile + mx_code_offset(p.r + i, lane >> 2) + 4 * (lane & 3));
-}
-
-__device__ __forceinline__ uint8_t *scale_byte(const Part &p, int i, int lane) {
-    return p.tile + mx_scale_offset(p.r + i, lane >> 4) + ((lane >> 2) & 3);
-}
-
-__device__ __forceinline__ uint32_t *scale_word(const Part &p, int lane) {
-    return reinterpret_cast<uint32_t *>(p.tile + mx_scale_offset(p.r + (lane >> 1), lane & 1));
+__device__ __forceinline__ uint32_t *code_word(const Part &p, int i) {
+    return reinterpret_cast<uint32_t *>(p.codes + 128 * i + (p.word ^ (i << 4)));
 }
 
 template <typename T, int ROWS>
@@ -65,11 +69,10 @@ __global__ void __launch_bounds__(32 * kWarps, 8)
     const int lane = threadIdx.x & 31;
     Part p;
     if (!part_of<ROWS>(p, W, R, K, kt)) return;
-    const int64_t at = p.row0 * K + p.k;
     Raw8<T> x[ROWS];
     #pragma unroll
     for (int i = 0; i < ROWS; ++i)
-        if (p.live && i < p.rows) x[i].load(X, at + i * K);
+        if (p.live && i < p.rows) x[i].load(X, p.at + i * K);
     #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         if (i < p.rows) {   // the same in all lanes
@@ -77,8 +80,8 @@ __global__ void __launch_bounds__(32 * kWarps, 8)
             if (p.live) x[i].get(v);
             uint32_t byte;
             const uint32_t code = mx_encode8(v, byte);
-            *code_word(p, i, lane) = code;
-            if ((lane & 3) == 0) *scale_byte(p, i, lane) = static_cast<uint8_t>(byte);   // 0 for a block past K
+            *code_word(p, i) = code;
+            if ((lane & 3) == 0) p.scale[16 * i] = static_cast<uint8_t>(byte);   // 0 for a block past K
         }
     }
 }
@@ -120,14 +123,16 @@ template <typename T, int ROWS>
 __global__ void __launch_bounds__(32 * kWarps) mx_dequant_kernel(const uint8_t *__restrict__ W, T *__restrict__ out, int64_t R,
                                                                  int64_t K, int kt) {
     begin_dependent();
-    const int lane = threadIdx.x & 31;
     Part p;
     if (!part_of<ROWS>(p, W, R, K, kt)) return;
     uint32_t code[ROWS];
     #pragma unroll
-    for (int i = 0; i < ROWS; ++i) code[i] = i < p.rows ? __ldcs(code_word(p, i, lane)) : 0u;
-    const uint32_t words = lane < 2 * p.rows ? __ldcs(scale_word(p, lane)) : 0u;
-    T *o = out + p.row0 * K + p.k;
+    for (int i = 0; i < ROWS; ++i) code[i] = i < p.rows ? __ldcs(code_word(p, i)) : 0u;
+    // lane 2i + g has the scales of row i's blocks 4g .. 4g+3
+    const int lane = threadIdx.x & 31;
+    const uint32_t words =
+        lane < 2 * p.rows ? __ldcs(reinterpret_cast<const uint32_t *>(p.scales + 16 * (lane >> 1) + 512 * (lane & 1))) : 0u;
+    T *o = out + p.at;
     #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const uint32_t word = __shfl_sync(0xffffffffu, words, 2 * i + (lane >> 4));
@@ -152,9 +157,9 @@ __global__ void __launch_bounds__(32 * kWarps) mx_pack_kernel(const uint8_t *__r
     #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         if (i < p.rows) {
-            const int64_t at = (p.row0 + i) * K + p.k;
-            *code_word(p, i, lane) = p.live ? __ldcs(reinterpret_cast<const uint32_t *>(codes + at / 2)) : 0u;
-            if ((lane & 3) == 0) *scale_byte(p, i, lane) = p.live ? scales[at / 32] : 0;
+            const int64_t at = p.at + i * K;
+            *code_word(p, i) = p.live ? __ldcs(reinterpret_cast<const uint32_t *>(codes + at / 2)) : 0u;
+            if ((lane & 3) == 0) p.scale[16 * i] = p.live ? scales[at / 32] : 0;
         }
     }
 }

@@ -183,7 +183,7 @@ __device__ __forceinline__ void store_mxfp4(const NormParams &P, int64_t row, co
             for (int h = 0; h < 2; ++h) {
                 const bool live = k + 128 * h < P.D;
                 const uint32_t byte = live ? mx_scale_byte(a[j][h]) : 0u;
-                const float inv = mx_inverse_scale(byte);
+                const float inv = mx_inverse_scale(a[j][h]);
                 const float *u = v[j] + 4 * h;
                 const uint32_t code = live ? e2m1x4(u[0] * inv, u[1] * inv, u[2] * inv, u[3] * inv) : 0u;
                 const int b = 4 * h + (lane >> 3);
