@@ -156,6 +156,24 @@ __device__ __forceinline__ void store_columns(const SplitParams &P, uint32_t d, 
     }
 }
 
+// A rank's columns [first, last): the ranks' sums of one weight row in rank
+// order, four columns at a time, whose loads do not wait for each other.
+template <class T>
+__device__ __forceinline__ void store_sums(const SplitParams &P, const float *red, int first, int last, int cpr, int64_t n) {
+    T *y = static_cast<T *>(P.Y) + first * P.N + n;
+    for (int c = first; c < last; c += 4) {
+        float sum[4] = {};
+        const float *p = red + (c - first) * 128;
+        for (int q = 0; q < P.split; ++q, p += cpr * 128)
+            #pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < last) sum[j] += p[j * 128];
+        #pragma unroll
+        for (int j = 0; j < 4; ++j, y += P.N)
+            if (c + j < last) put(y, sum[j]);
+    }
+}
+
 __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_constant__ SplitParams P) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ SplitSmem S;
@@ -288,14 +306,9 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
                                  remote_addr(smem_addr(&S.red_full), lane))
                              : "memory");
             if (rank * cpr < live && wait_or_abort<true>(&S.red_full, 0, &S.abort_flag, P.err) && n < P.N) {
-                #pragma unroll 1
-                for (int c = rank * cpr; c < live && c < (rank + 1) * cpr; ++c) {
-                    const float *p = red + (c - rank * cpr) * 128 + row;
-                    float v = 0.f;
-                    for (int q = 0; q < P.split; ++q) v += p[q * cpr * 128];
-                    if (P.bf16) put(static_cast<__nv_bfloat16 *>(P.Y) + c * P.N + n, v);
-                    else put(static_cast<float *>(P.Y) + c * P.N + n, v);
-                }
+                const int first = rank * cpr, last = min(first + cpr, live);
+                if (P.bf16) store_sums<__nv_bfloat16>(P, red + row, first, last, cpr, n);
+                else store_sums<float>(P, red + row, first, last, cpr, n);
             }
         }
     }
@@ -326,16 +339,29 @@ cudaError_t launch_split(const uint8_t *W, const uint8_t *X, void *Y, bool bf16,
     if (e != cudaSuccess) return e;
     const int kt = static_cast<int>(kt64), xcap = static_cast<int>(M + 7) & ~7;
     const int64_t tiles = q4::mx_row_tiles(N);
-    // K is split into as many parts as leave each CTA an SM of its own, with
-    // four steps or more a part: below, meeting in shared memory (0.5 us) costs more than it
-    // saves.  Measured, us: 1 x 5120 x 8192 11.1 whole, 8.6 in 2, 7.3 in 3
-    // (the rule), 8.3 in 4; 2 x 5120 x 4096 7.2, 6.4, 5.8, 6.0; 4 x 2048 x 8192
-    // 11.2 whole, 5.0 in 8 (the rule); 32 x 16384 x 5120 10.5 whole (the rule),
-    // 13.5 in 2; 1 x 1024 x 1024 2.8 whole (the rule), 3.3 in 4.
-    int split = static_cast<int>(dev.sm_count / tiles);
-    if (split > kt / 4) split = kt / 4;
-    if (split > 8) split = 8;
-    if (split < 1) split = 1;
+    // K is split into the number of parts that a model of the time favours, of
+    // those that leave each CTA an SM of its own.  The model's figures (ns)
+    // are fits to measured times: a step costs 170 while it was loaded at once
+    // with the others, 110 more (220 in the smaller ring of a split CTA) once
+    // slots are reused, HBM passes 6400 bytes, and the meeting of the sums
+    // takes 400 and more with the CTAs and the rows.  Measured, us, whole and
+    // split: 1 x 5120 x 8192 11.0 and 7.4 (3 parts), 1 x 256 x 5120 7.1 and 3.7 (8),
+    // 32 x 5120 x 5120 8.1 and 6.9 (3), 16 x 1024 x 2048 4.0 and 3.8 (8); whole by
+    // the rule: 16 x 5120 x 2048 4.2 and 4.9 (3), 32 x 16384 x 5120 9.7.
+    const int64_t hbm = tiles * kt * kMxTileBytes / 6400;
+    int split = 1;
+    int64_t least = 0;
+    for (int parts = 1; parts <= 8 && parts <= kt && (parts == 1 || tiles * parts <= dev.sm_count); ++parts) {
+        if (parts == 5 || parts == 7) continue;   // slower than their neighbours (32 x 1024 x 5120: 7 parts 5.4 us, 8 4.8)
+        const int64_t steps = (kt + parts - 1) / parts, ring = parts == 1 ? 9 : 5;
+        int64_t cost = 170 * steps + (steps > ring ? (parts == 1 ? 110 : 220) * (steps - ring) : 0);
+        if (cost < hbm) cost = hbm;
+        if (parts > 1) cost += 400 + 3 * tiles * parts + 25 * M;
+        if (parts == 1 || cost < least) {
+            split = parts;
+            least = cost;
+        }
+    }
     // a CTA that has its SM to itself takes the memory of two; split ones leave
     // room for the next launch's CTAs
     const int budget = split == 1 && tiles <= dev.sm_count ? kSplitSmemMax : kSplitSmemHalf;
@@ -359,7 +385,7 @@ cudaError_t launch_split(const uint8_t *W, const uint8_t *X, void *Y, bool bf16,
     attr[1].val.clusterDim.x = split;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, mx_split_kernel, p);
 }
 
