@@ -37,19 +37,21 @@ Q4_0_API int64_t mxfp4_bytes(int64_t R, int64_t K);
  * of zeros: -127); codes x * 2^-E to the nearest E2M1 number, ties to the
  * even code, magnitudes above 6 to 6.  A block that holds an infinity or a
  * NaN gets scale byte 255.  Deterministic and bit-exact.  X and W 16-byte
- * aligned, K % 32 == 0; R == 0 or K == 0 writes nothing. */
+ * aligned and not overlapping, K % 32 == 0; R == 0 or K == 0 writes nothing. */
 Q4_0_API int mxfp4_quantize(const void *X, int x_type, void *W, int64_t R, int64_t K, q4_0_stream_t stream);
 
 /* The values an MXFP4 matrix stands for, out [R,K] row-major in fp32, bf16 or
  * fp16 (out_type).  Exact in fp32 and bf16 (a code has two significant bits
- * and the exponents fit); rounded once, to nearest even, in fp16. */
+ * and the exponents fit); rounded once, to nearest even, in fp16.
+ * W and out 16-byte aligned and not overlapping. */
 Q4_0_API int mxfp4_dequant(const void *W, void *out, int out_type, int64_t R, int64_t K, q4_0_stream_t stream);
 
 /* Codes and scales as checkpoints hold them into the layout above (bit-exact):
  *   codes  [R,K/2] uint8 row-major, two codes to a byte, the lower k in the
  *          low bits;
  *   scales [R,K/32] uint8 row-major, E + 127 (255: NaN).
- * All pointers 16-byte aligned; R == 0 or K == 0 writes nothing. */
+ * All pointers 16-byte aligned, W overlapping neither of the others; R == 0 or
+ * K == 0 writes nothing. */
 Q4_0_API int mxfp4_pack(const uint8_t *codes, const uint8_t *scales, void *W, int64_t R, int64_t K, q4_0_stream_t stream);
 
 /* Y[M,N] = X[M,K] * W[N,K]^T of two MXFP4 matrices, Y row-major in fp32 or

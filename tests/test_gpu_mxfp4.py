@@ -171,6 +171,33 @@ def test_gemm_nan_block_marks_its_row_and_column_only(q4):
     assert np.array_equal(nan, want)
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 70, 288), (33, 200, 544), (130, 300, 1056), (300, 40, 288)])
+def test_gemm_does_not_look_at_rows_past_the_last(q4, M, N, K):
+    """Memory behind the last rows may hold anything: NaN scales here, and no
+    row or column of the result knows of them."""
+    rng = np.random.default_rng(M)
+    mats = []
+    for R in (N, M):
+        codes = rng.integers(0, 16, (R, K), dtype=np.uint8)
+        scales = rng.integers(121, 133, (R, K // 32), dtype=np.uint8)
+        B = torch.full((q4.mxfp4_bytes(R, K),), 0xFF, dtype=torch.uint8, device="cuda")
+        q4.mxfp4_pack(torch.from_numpy(ref.packed(codes)).cuda(), torch.from_numpy(scales).cuda(), B, R, K)
+        mats.append((ref.values(codes, scales), B))
+    Y = torch.empty((M, N), device="cuda")
+    q4.mxfp4_gemm(mats[0][1], mats[1][1], Y, M, N, K)
+    _check_product(Y, mats[1][0], mats[0][0], K)
+
+
+def test_gemm_on_the_first_rows_of_a_larger_matrix(q4):
+    rng = np.random.default_rng(8)
+    x, X = _random_matrix(q4, rng, 300, 512)
+    w, W = _random_matrix(q4, rng, 200, 512)
+    for M, N in ((1, 200), (130, 129), (299, 1)):
+        Y = torch.empty((M, N), device="cuda")
+        q4.mxfp4_gemm(W, X, Y, M, N, 512)
+        _check_product(Y, x[:M], w[:N], 512)
+
+
 def test_gemm_of_nothing(q4):
     W = torch.empty(0, dtype=torch.uint8, device="cuda")
     Y = torch.full((3, 5), 7.0, device="cuda")
