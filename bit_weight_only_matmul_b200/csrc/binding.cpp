@@ -120,7 +120,7 @@ class Call {
             return refuse("%s: on device %d, the current device is %d", what, static_cast<int>(t.get_device()), static_cast<int>(device_));
         const int k = type_of(t);
         if (k < 0 || !(types >> k & 1)) return refuse("%s: dtype %s is not supported here", what, c10::toString(t.scalar_type()));
-        if (!t.is_contiguous()) return refuse("%s: expected a contiguous tensor", what);
+        if (t.is_nested() || !t.is_contiguous()) return refuse("%s: expected a contiguous tensor", what);
         if (type) *type = k;
         return &t;
     }
@@ -224,7 +224,21 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return status(c, [&] { return q4_0_block_norm(&b, s); });
 }
 
-#define METHOD(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
+// A tensor without plain storage (sparse, fake) throws when it is asked
+// for its strides or its address: an error of the caller's, not the process's end.
+template <PyObject *F(PyObject *, PyObject *const *, Py_ssize_t)>
+PyObject *guarded(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    try {
+        return F(self, a, n);
+    } catch (const c10::Error &e) {
+        PyErr_Format(PyExc_ValueError, "expected tensors with storage: %s", e.what_without_backtrace());
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+    }
+    return nullptr;
+}
+
+#define METHOD(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<f>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {METHOD("mxfp4_quantize", quantize), METHOD("mxfp4_dequant", dequant), METHOD("mxfp4_pack", pack),
                            METHOD("mxfp4_gemm", gemm), METHOD("q4_0_block_norm", block_norm), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -171,6 +171,33 @@ def test_gemm_nan_block_marks_its_row_and_column_only(q4):
     assert np.array_equal(nan, want)
 
 
+@pytest.mark.parametrize("M", [17, 40, 255])
+@pytest.mark.parametrize("cx,cw", [(1, 1), (1, 7), (7, 2)])
+def test_gemm_over_the_whole_range_of_scales(q4, M, cx, cw):
+    """One product a sum, of all pairs of scales 2^-127 .. 2^127: exact wherever
+    fp32 has the number as a normal one, infinite above."""
+    K, w_exp = 64, np.arange(255)
+    x_exp = w_exp[:: 255 // M][:M]
+
+    def matrix(exps, code):
+        codes = np.zeros((len(exps), K), np.uint8)
+        scales = np.full((len(exps), 2), 127, np.uint8)
+        codes[:, 5], scales[:, 0] = code, exps
+        B = _matrix(q4, len(exps), K)
+        q4.mxfp4_pack(torch.from_numpy(ref.packed(codes)).cuda(), torch.from_numpy(scales).cuda(), B, len(exps), K)
+        return B
+    W, X = matrix(w_exp, cw), matrix(x_exp, cx)
+    Y = torch.empty((M, 255), device="cuda")
+    q4.mxfp4_gemm(W, X, Y, M, 255, K)
+    value = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6])
+    want = value[cx] * value[cw] * np.exp2(x_exp[:, None] - 127.0) * np.exp2(w_exp[None, :] - 127.0)
+    got = Y.double().cpu().numpy()
+    normal, above = (want >= 2.0 ** -126) & (want < 2.0 ** 128), want >= 2.0 ** 128
+    assert np.array_equal(got[normal], want[normal])
+    assert np.isposinf(got[above]).all()
+    assert (got[want < 2.0 ** -126] < 2.0 ** -126).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 70, 288), (33, 200, 544), (130, 300, 1056), (300, 40, 288)])
 def test_gemm_does_not_look_at_rows_past_the_last(q4, M, N, K):
     """Memory behind the last rows may hold anything: NaN scales here, and no
@@ -224,3 +251,19 @@ def test_binding_refusals(q4):
         q4.mxfp4_quantize(x, W, 2, 40)
     with pytest.raises(ValueError, match="dtype"):
         q4.q4_0_block_norm(x, R, K, r_out=x.bfloat16())
+
+
+def test_binding_refuses_tensors_without_plain_storage(q4):
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    R, K = 4, 64
+    x = torch.ones((R, K), device="cuda")
+    W = _matrix(q4, R, K)
+    with FakeTensorMode():
+        fake = torch.empty((R, K), device="cuda")
+    for bad in (x.to_sparse(), torch.nested.nested_tensor([x, x]), fake):
+        for call in (lambda: q4.mxfp4_quantize(bad, W, R, K), lambda: q4.mxfp4_dequant(W, bad, R, K),
+                     lambda: q4.mxfp4_gemm(W, W, bad, R, R, K), lambda: q4.q4_0_block_norm(bad, R, K, x=x),
+                     lambda: q4.q4_0_block_norm(x, R, K, x=bad)):
+            with pytest.raises((ValueError, RuntimeError)):
+                call()
+    assert torch.equal(x, torch.ones_like(x))
