@@ -42,7 +42,8 @@ Q4_0_API int mxfp4_quantize(const void *X, int x_type, void *W, int64_t R, int64
 
 /* The values an MXFP4 matrix stands for, out [R,K] row-major in fp32, bf16 or
  * fp16 (out_type).  Exact in fp32 and bf16 (a code has two significant bits
- * and the exponents fit); rounded once, to nearest even, in fp16.
+ * and the exponents fit, but for codes from 2 on at the largest scales, above
+ * the type's range: infinity); rounded once, to nearest even, in fp16.
  * W and out 16-byte aligned and not overlapping. */
 Q4_0_API int mxfp4_dequant(const void *W, void *out, int out_type, int64_t R, int64_t K, q4_0_stream_t stream);
 
@@ -55,11 +56,11 @@ Q4_0_API int mxfp4_dequant(const void *W, void *out, int out_type, int64_t R, in
 Q4_0_API int mxfp4_pack(const uint8_t *codes, const uint8_t *scales, void *W, int64_t R, int64_t K, q4_0_stream_t stream);
 
 /* Y[M,N] = X[M,K] * W[N,K]^T of two MXFP4 matrices, Y row-major in fp32 or
- * bf16 (y_type), overwritten.  Products are exact and sums fp32; a bf16 Y is
- * rounded once.  The same inputs give the same bits.  W, X, Y 16-byte
- * aligned, Y not overlapping W or X; K % 32 == 0.  M == 0 or N == 0 does
- * nothing; K == 0 fills Y with zeros.  A NaN block makes its row (of X) or
- * column (of W) of Y NaN. */
+ * bf16 (y_type), overwritten.  Products are exact within fp32's normal range
+ * and sums fp32; a bf16 Y is rounded once.  The same inputs give the same
+ * bits.  W, X, Y 16-byte aligned, Y not overlapping W or X; K % 32 == 0.
+ * M == 0 or N == 0 does nothing; K == 0 fills Y with zeros.  A NaN block makes
+ * its row (of X) or column (of W) of Y NaN. */
 Q4_0_API int mxfp4_gemm(const void *W, const void *X, void *Y, int y_type, int64_t M, int64_t N, int64_t K,
                         q4_0_stream_t stream);
 

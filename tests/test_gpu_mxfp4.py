@@ -78,6 +78,19 @@ def test_quantize_ends_of_the_range(q4):
     assert torch.isnan(out[-3:, :32]).all() and torch.isfinite(out[-3:, 32:]).all()
 
 
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16, torch.float16])
+def test_dequant_of_every_code_and_scale(q4, t):
+    codes = np.tile(np.arange(32, dtype=np.uint8) % 16, (256, 1))
+    scales = np.arange(256, dtype=np.uint8)[:, None]
+    W, out = _matrix(q4, 256, 32), torch.empty((256, 32), dtype=t, device="cuda")
+    q4.mxfp4_pack(torch.from_numpy(ref.packed(codes)).cuda(), torch.from_numpy(scales).cuda(), W, 256, 32)
+    q4.mxfp4_dequant(W, out, 256, 32)
+    want = torch.from_numpy(ref.values(codes, scales)).to(t)
+    got = out.cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.isnan(got[255]).all()
+    assert torch.equal(got[:255], want[:255])
+
+
 @pytest.mark.parametrize("R,K", [(1, 32), (7, 96), (130, 288), (256, 512)])
 def test_pack_bit_exact(q4, R, K):
     rng = np.random.default_rng(R + K)
