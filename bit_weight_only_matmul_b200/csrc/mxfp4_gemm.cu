@@ -19,7 +19,7 @@
 //     rate), where a loop under `if (lane == 0)` took 733 and 738;
 //   * epilogue warps that drain the accumulator and store Y.
 // mx_split_kernel (few rows) is paced by the weight stream from HBM: 1 x 131072 x
-// 5120 54.7 us, 6.5 TB/s; 32 x 16384 x 5120 10.3 us, of which 4 are start and end.
+// 5120 54.7 us, 6.5 TB/s; 32 x 16384 x 5120 9.7 us, of which 4 are start and end.
 // mx_pair_kernel (many) is paced by the tensor cores under the power cap: 4096 x
 // 16384 x 5120 with bf16 Y 125 us, 5.5 PFLOP/s.
 #include <cstring>
@@ -95,7 +95,7 @@ __device__ __forceinline__ bool elect_one() {
 // ---------------------------------------------------------------- few rows
 
 // The split kernel: a cluster of `split` CTAs takes 128 weight rows and all
-// activation rows (up to 32), each CTA a run of the 256-k steps.  The ranks'
+// activation rows (up to 128), each CTA a run of the 256-k steps.  The ranks'
 // sums meet in shared memory: rank q adds columns [q*cpr, (q+1)*cpr) over all
 // ranks, in rank order, so the result does not depend on timing.
 struct SplitParams {
@@ -341,30 +341,31 @@ cudaError_t launch_split(const uint8_t *W, const uint8_t *X, void *Y, bool bf16,
     const int64_t tiles = q4::mx_row_tiles(N);
     // K is split into the number of parts that a model of the time favours, of
     // those that leave each CTA an SM of its own.  The model's figures (ns)
-    // are fits to measured times: a step costs 170 while it was loaded at once
-    // with the others, 110 more (220 in the smaller ring of a split CTA) once
-    // slots are reused, HBM passes 6400 bytes, and the meeting of the sums
-    // takes 400 and more with the CTAs and the rows.  Measured, us, whole and
-    // split: 1 x 5120 x 8192 11.0 and 7.4 (3 parts), 1 x 256 x 5120 7.1 and 3.7 (8),
-    // 32 x 5120 x 5120 8.1 and 6.9 (3), 16 x 1024 x 2048 4.0 and 3.8 (8); whole by
-    // the rule: 16 x 5120 x 2048 4.2 and 4.9 (3), 32 x 16384 x 5120 9.7.
+    // are fits to measured times: a step costs 155 and 0.5 a row while it was
+    // loaded at once with the others, 110 more (220 in the smaller ring of a
+    // split CTA) once slots are reused, HBM passes 6400 bytes, and the meeting
+    // of the sums takes 400 and more with the rows and the CTAs.  Measured, us,
+    // whole and split: 1 x 5120 x 8192 11.0 and 7.4 (3 parts), 1 x 256 x 5120 7.1
+    // and 3.7 (8), 32 x 5120 x 5120 8.1 and 6.9 (3), 16 x 1024 x 2048 4.0 and
+    // 3.8 (8), 64 x 5120 x 8192 11.9 and 10.0 (3); whole by the rule: 16 x 5120 x
+    // 2048 4.2 and 4.9 (3), 32 x 16384 x 5120 9.7, 128 x 5120 x 5120 9.5 and 10.6 (3).
     const int64_t hbm = tiles * kt * kMxTileBytes / 6400;
     int split = 1;
     int64_t least = 0;
     for (int parts = 1; parts <= 8 && parts <= kt && (parts == 1 || tiles * parts <= dev.sm_count); ++parts) {
         if (parts == 5 || parts == 7) continue;   // slower than their neighbours (32 x 1024 x 5120: 7 parts 5.4 us, 8 4.8)
         const int64_t steps = (kt + parts - 1) / parts, ring = parts == 1 ? 9 : 5;
-        int64_t cost = 170 * steps + (steps > ring ? (parts == 1 ? 110 : 220) * (steps - ring) : 0);
+        int64_t cost = (155 + M / 2) * steps + (steps > ring ? (parts == 1 ? 110 : 220) * (steps - ring) : 0);
         if (cost < hbm) cost = hbm;
-        if (parts > 1) cost += 400 + 3 * tiles * parts + 25 * M;
+        if (parts > 1) cost += 400 + 20 * M + tiles * parts * (30 + M) / 10;
         if (parts == 1 || cost < least) {
             split = parts;
             least = cost;
         }
     }
-    // a CTA that has its SM to itself takes the memory of two; split ones leave
-    // room for the next launch's CTAs
-    const int budget = split == 1 && tiles <= dev.sm_count ? kSplitSmemMax : kSplitSmemHalf;
+    // a CTA that has its SM to itself takes the memory of two, but where a few
+    // rows' split ones do with less and leave room for the next launch's CTAs
+    const int budget = tiles <= dev.sm_count && (split == 1 || M > 32) ? kSplitSmemMax : kSplitSmemHalf;
     const int need = (kt + split - 1) / split, red = split_red_bytes(xcap, split);
     int slots = (budget - 1024 - red) / split_slot_bytes(xcap);
     if (slots > (kSplitTmemCols - split_d_cols(xcap)) / 16) slots = (kSplitTmemCols - split_d_cols(xcap)) / 16;
@@ -658,11 +659,12 @@ cudaError_t launch_mx_gemm(const uint8_t *W, const uint8_t *X, void *Y, int y_ty
                            const DeviceInfo &dev, cudaStream_t s) {
     const int64_t kt = mx_k_tiles(K), wt = mx_row_tiles(N), xt = mx_row_tiles(M);
     const bool bf16 = y_type == Q4_TYPE_BF16;
-    // up to 32 rows the weight stream paces both kernels, and splitting K uses
-    // more SMs; above, the pair kernel is ahead (us, split and pair: 16 x 16384
-    // x 5120 9.7 and 10.8, 32 x 16384 x 5120 10.9 and 10.8, 64 x 16384 x 5120
-    // 12.4 and 10.9, 16 x 5120 x 8192 8.4 and 11.1, 64 x 5120 x 8192 12.7 and 11.3)
-    if (M <= 32) return launch_split(W, X, Y, bf16, M, N, kt, dev, s);
+    // up to 128 rows, one tile of X, the pair kernel's weight tiles are as many
+    // but go to half as many places, and it cannot split K (us, split and pair:
+    // 64 x 16384 x 5120 10.2 and 10.9, 64 x 5120 x 8192 10.0 and 11.4, 64 x 1024 x 5120
+    // 5.7 and 8.3, 64 x 32768 x 5120 16.9 and 21.2, 128 x 16384 x 5120 11.1 and 11.5,
+    // 128 x 2048 x 2048 5.6 and 6.2; the other way 128 x 8192 x 5120 9.8 and 9.5)
+    if (M <= q4::kMxTileRows) return launch_split(W, X, Y, bf16, M, N, kt, dev, s);
     const int64_t tiles_n = (wt + 1) / 2;
     // tiles of 128 activation rows while they all run at once, of 256 beyond
     // (us, 128 and 256: 333 x 5003 x 4128 9.0 and 11.3, 512 x 2048 x 2048 6.2 and
