@@ -200,9 +200,15 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
     }
     if (warp >= 2 && lane == 0) {
         // the first weight tiles on their way to L2 while the kernel before
-        // this one ends
+        // this one ends: as many as the ring takes where K is short or split
+        // (behind a norm, 2 x 5120 x 4096 8.6 us without, 8.1 with; behind a
+        // quantize, 8 x 8192 x 2048 6.1 and 5.6).  A whole K of more steps soon
+        // keeps HBM busy, and copies that wait for a prefetch cost more than
+        // others: two tiles (behind a quantize, 32 x 16384 x 5120 11.5 us without,
+        // 11.3 with two tiles, 12.5 with nine)
+        const int ahead = P.split == 1 && P.kt > P.slots ? min(2, P.slots) : P.slots;
         const uint8_t *w = P.W + (static_cast<int64_t>(tn) * P.kt + k0) * kMxTileBytes;
-        for (int i = warp - 2; i < P.slots && k0 + i < k1; i += 5) bulk_prefetch_l2(w + static_cast<int64_t>(i) * kMxTileBytes, kMxTileBytes);
+        for (int i = warp - 2; i < ahead && k0 + i < k1; i += 5) bulk_prefetch_l2(w + static_cast<int64_t>(i) * kMxTileBytes, kMxTileBytes);
     }
     if (warp == 1) tmem_alloc(&S.tmem_base, kSplitTmemCols);
     tc_fence_before();
