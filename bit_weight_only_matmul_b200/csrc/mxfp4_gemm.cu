@@ -97,7 +97,9 @@ __device__ __forceinline__ bool elect_one() {
 // The split kernel: a cluster of `split` CTAs takes 128 weight rows and all
 // activation rows (up to 128), each CTA a run of the 256-k steps.  The ranks'
 // sums meet in shared memory: rank q adds columns [q*cpr, (q+1)*cpr) over all
-// ranks, in rank order, so the result does not depend on timing.
+// ranks, in rank order, so the result does not depend on timing.  They travel
+// in groups of four columns, 16 bytes a lane (128 x 1024 x 5120 8.4 us one by one,
+// 7.7 in groups), one or two columns one by one (1 x 5120 x 8192 7.2 and 7.3).
 struct SplitParams {
     const uint8_t *W, *X;
     void *Y;
@@ -123,10 +125,10 @@ struct SplitSmem {
 
 __host__ __device__ constexpr int split_x_bytes(int xcap) { return (xcap * 128 + 1023) & ~1023; }
 __host__ __device__ constexpr int split_slot_bytes(int xcap) { return kMxTileBytes + split_x_bytes(xcap) + 1024; }
-// the ranks' sums of one rank's columns, [source rank][column][weight row]
-__host__ __device__ constexpr int split_red_bytes(int xcap, int split) {
-    return split > 1 ? split * ((xcap + split - 1) / split) * 512 : 0;
-}
+// columns a rank adds, in whole groups of four
+__host__ __device__ constexpr int split_cpr(int xcap, int split) { return ((xcap + split - 1) / split + 3) & ~3; }
+// the ranks' sums of one rank's columns, [source rank][group][weight row][column of the group]
+__host__ __device__ constexpr int split_red_bytes(int xcap, int split) { return split > 1 ? split * split_cpr(xcap, split) * 512 : 0; }
 __host__ __device__ constexpr int split_d_cols(int xcap) { return (xcap + 15) & ~15; }
 
 __device__ __forceinline__ void cluster_sync_all() {
@@ -156,21 +158,70 @@ __device__ __forceinline__ void store_columns(const SplitParams &P, uint32_t d, 
     }
 }
 
+// A warp's 32 lanes of the accumulator to the ranks that add their columns, in
+// groups of G; `mine` is the lane's row in this rank's first group.
+template <int G>
+__device__ __forceinline__ void send_columns(int live, int cpr, uint32_t d, uint32_t mine) {
+    int dest = 0, at = 0;
+    #pragma unroll 1
+    for (int c = 0; c < live; c += 8) {
+        float v[8];
+        tc_ld_cols<8>(d + c, v);
+        tc_wait_ld();
+        #pragma unroll
+        for (int j = 0; j < 8; j += G) {
+            if (c + j < live) {
+                const uint32_t to = remote_addr(mine + at * 512, dest);
+                if constexpr (G == 4)
+                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v[j]), "f"(v[j + 1]),
+                                 "f"(v[j + 2]), "f"(v[j + 3])
+                                 : "memory");
+                else
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v[j]) : "memory");
+            }
+            if ((at += G) == cpr) { at = 0; ++dest; }
+        }
+    }
+}
+
 // A rank's columns [first, last): the ranks' sums of one weight row in rank
-// order, four columns at a time, whose loads do not wait for each other.
-template <class T>
+// order.  `red` is that row's place in the first group of the first rank.
+template <int G, class T>
 __device__ __forceinline__ void store_sums(const SplitParams &P, const float *red, int first, int last, int cpr, int64_t n) {
     T *y = static_cast<T *>(P.Y) + first * P.N + n;
-    for (int c = first; c < last; c += 4) {
-        float sum[4] = {};
-        const float *p = red + (c - first) * 128;
-        for (int q = 0; q < P.split; ++q, p += cpr * 128)
-            #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c + j < last) sum[j] += p[j * 128];
+    for (int c = first; c < last; c += G, red += G * 128) {
+        float sum[G] = {};
+        const float *p = red;
+        for (int q = 0; q < P.split; ++q, p += cpr * 128) {
+            if constexpr (G == 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(p);
+                sum[0] += v.x; sum[1] += v.y; sum[2] += v.z; sum[3] += v.w;
+            } else {
+                sum[0] += *p;
+            }
+        }
         #pragma unroll
-        for (int j = 0; j < 4; ++j, y += P.N)
+        for (int j = 0; j < G; ++j, y += P.N)
             if (c + j < last) put(y, sum[j]);
+    }
+}
+
+// A warp's part in the meeting of the sums.
+template <int G>
+__device__ __forceinline__ void meet(const SplitParams &P, SplitSmem &S, float *red, int rank, int row, uint32_t d, int64_t n) {
+    const int cpr = split_cpr(P.xcap, P.split);
+    send_columns<G>(P.M, cpr, d, smem_addr(red + rank * cpr * 128 + G * row));
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    __syncwarp();
+    const int lane = threadIdx.x & 31;
+    if (lane < P.split)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                         remote_addr(smem_addr(&S.red_full), lane))
+                     : "memory");
+    if (rank * cpr < P.M && wait_or_abort<true>(&S.red_full, 0, &S.abort_flag, P.err) && n < P.N) {
+        const int first = rank * cpr, last = min(first + cpr, P.M);
+        if (P.bf16) store_sums<G, __nv_bfloat16>(P, red + G * row, first, last, cpr, n);
+        else store_sums<G, float>(P, red + G * row, first, last, cpr, n);
     }
 }
 
@@ -183,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
     float *const red = reinterpret_cast<float *>(ring + P.slots * slot_bytes);
     const int rank = static_cast<int>(blockIdx.x) % P.split;      // clusters are consecutive blocks
     const int tn = static_cast<int>(blockIdx.x) / P.split;
-    const int live = P.M, rows = P.xcap;
+    const int rows = P.xcap;
     const int k0 = static_cast<int>(static_cast<int64_t>(P.kt) * rank / P.split);
     const int k1 = static_cast<int>(static_cast<int64_t>(P.kt) * (rank + 1) / P.split);
 
@@ -288,34 +339,10 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
         if (P.split == 1) {
             if (P.bf16) store_columns<__nv_bfloat16>(P, d, n);
             else store_columns<float>(P, d, n);
+        } else if (P.M <= 2) {
+            meet<1>(P, S, red, rank, row, d, n);
         } else {
-            const int cpr = (P.xcap + P.split - 1) / P.split;   // columns a rank adds
-            const uint32_t mine = smem_addr(red + rank * cpr * 128 + row);
-            int dest = 0, at = 0;
-            #pragma unroll 1
-            for (int c = 0; c < live; c += 8) {
-                float v[8];
-                tc_ld_cols<8>(d + c, v);
-                tc_wait_ld();
-                #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (c + j < live)
-                        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote_addr(mine + at * 512, dest)), "f"(v[j])
-                                     : "memory");
-                    if (++at == cpr) { at = 0; ++dest; }
-                }
-            }
-            asm volatile("fence.acq_rel.cluster;" ::: "memory");
-            __syncwarp();
-            if (lane < P.split)
-                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                                 remote_addr(smem_addr(&S.red_full), lane))
-                             : "memory");
-            if (rank * cpr < live && wait_or_abort<true>(&S.red_full, 0, &S.abort_flag, P.err) && n < P.N) {
-                const int first = rank * cpr, last = min(first + cpr, live);
-                if (P.bf16) store_sums<__nv_bfloat16>(P, red + row, first, last, cpr, n);
-                else store_sums<float>(P, red + row, first, last, cpr, n);
-            }
+            meet<4>(P, S, red, rank, row, d, n);
         }
     }
     __syncwarp();
@@ -336,6 +363,29 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
 // another cluster that waits for it.
 constexpr int kSplitSmemMax = 220 * 1024, kSplitSmemHalf = 111 * 1024, kSplitSmemMin = 80 * 1024;
 
+// Clusters of `parts` CTAs with an SM each that run at one time: a cluster lies
+// within a group of SMs, whose number need not be a multiple of it (128 x 2048 x
+// 5120 in 16 clusters of 8, two waves: 14.8 us, in clusters of 4 7.9).
+int clusters_at_once(int parts, const q4::DeviceInfo &dev) {
+    static q4::DeviceValue resident[9];
+    return resident[parts].get(dev.device, [&] {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = parts;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(dev.sm_count / parts * parts);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSplitSmemMax;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, mx_split_kernel, &cfg) != cudaSuccess) n = 0;
+        (void)cudaGetLastError();
+        return n > 0 ? n : 1;
+    });
+}
+
 cudaError_t launch_split(const uint8_t *W, const uint8_t *X, void *Y, bool bf16, int64_t M, int64_t N, int64_t kt64,
                          const q4::DeviceInfo &dev, cudaStream_t s) {
     static q4::DeviceOnce configured;
@@ -346,24 +396,21 @@ cudaError_t launch_split(const uint8_t *W, const uint8_t *X, void *Y, bool bf16,
     const int kt = static_cast<int>(kt64), xcap = static_cast<int>(M + 7) & ~7;
     const int64_t tiles = q4::mx_row_tiles(N);
     // K is split into the number of parts that a model of the time favours, of
-    // those that leave each CTA an SM of its own.  The model's figures (ns)
-    // are fits to measured times: a step costs 155 and 0.5 a row while it was
-    // loaded at once with the others, 110 more (220 in the smaller ring of a
-    // split CTA) once slots are reused, HBM passes 6400 bytes, and the meeting
-    // of the sums takes 400 and more with the rows and the CTAs.  Measured, us,
-    // whole and split: 1 x 5120 x 8192 11.0 and 7.4 (3 parts), 1 x 256 x 5120 7.1
-    // and 3.7 (8), 32 x 5120 x 5120 8.1 and 6.9 (3), 16 x 1024 x 2048 4.0 and
-    // 3.8 (8), 64 x 5120 x 8192 11.9 and 10.0 (3); whole by the rule: 16 x 5120 x
-    // 2048 4.2 and 4.9 (3), 32 x 16384 x 5120 9.7, 128 x 5120 x 5120 9.5 and 10.6 (3).
-    const int64_t hbm = tiles * kt * kMxTileBytes / 6400;
+    // those that leave each CTA an SM of its own and run all at once.  The model
+    // (ns) is a fit to 150 shapes, each with every number of parts: a step of
+    // a CTA costs 260 and two thirds of a row, the meeting of the sums 800 and
+    // more with the rows and the CTAs; on 150 others its choice is 0.9 % slower
+    // than the best on average, 11 % at worst.  Measured, us, whole and split: 1 x 5120 x 8192 11.0
+    // and 7.2 (3 parts), 1 x 256 x 5120 7.1 and 3.6 (8), 16 x 4096 x 4096 6.8 and
+    // 5.3 (4), 64 x 1024 x 5120 8.2 and 5.6 (8); whole by the rule: 16 x 5120 x 2048
+    // 4.2 and 4.9 (3), 128 x 5120 x 5120 9.5 and 10.6 (3).
     int split = 1;
     int64_t least = 0;
     for (int parts = 1; parts <= 8 && parts <= kt && (parts == 1 || tiles * parts <= dev.sm_count); ++parts) {
         if (parts == 5 || parts == 7) continue;   // slower than their neighbours (32 x 1024 x 5120: 7 parts 5.4 us, 8 4.8)
-        const int64_t steps = (kt + parts - 1) / parts, ring = parts == 1 ? 9 : 5;
-        int64_t cost = (155 + M / 2) * steps + (steps > ring ? (parts == 1 ? 110 : 220) * (steps - ring) : 0);
-        if (cost < hbm) cost = hbm;
-        if (parts > 1) cost += 400 + 20 * M + tiles * parts * (30 + M) / 10;
+        if (parts > 1 && M > 32 && tiles > clusters_at_once(parts, dev)) continue;
+        int64_t cost = (260 + 2 * M / 3) * ((kt + parts - 1) / parts);
+        if (parts > 1) cost += 800 + 20 * M + tiles * parts * (40 + M) / 10;
         if (parts == 1 || cost < least) {
             split = parts;
             least = cost;

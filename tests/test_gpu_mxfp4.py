@@ -129,7 +129,8 @@ SHAPES = [(1, 1, 32), (1, 128, 256), (1, 5120, 1024), (2, 129, 288), (7, 300, 54
           (300, 77, 4128), (513, 1290, 640), (3, 16400, 512), (17, 128, 8192), (65, 700, 2560), (128, 1024, 4096),
           (16, 40000, 288), (90, 20000, 320), (1000, 2050, 1056), (2500, 2600, 320),
           (385, 5000, 2080), (1100, 2304, 512), (33, 1, 32), (48, 5200, 1024), (20, 2048, 8192),
-          (127, 1000, 5120), (64, 5120, 5120), (72, 130, 8192), (113, 20000, 1056), (121, 257, 4096), (44, 5003, 8160)]
+          (127, 1000, 5120), (64, 5120, 5120), (72, 130, 8192), (113, 20000, 1056), (121, 257, 4096), (44, 5003, 8160),
+          (33, 2304, 8192), (128, 2048, 5120), (3, 2100, 8192), (50, 300, 2048), (1, 4096, 4096), (2, 1000, 5120)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
