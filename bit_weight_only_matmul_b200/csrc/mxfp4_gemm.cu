@@ -19,7 +19,7 @@
 //     rate), where a loop under `if (lane == 0)` took 733 and 738;
 //   * epilogue warps that drain the accumulator and store Y.
 // mx_split_kernel (few rows) is paced by the weight stream from HBM: 1 x 131072 x
-// 5120 54.7 us, 6.5 TB/s; 32 x 16384 x 5120 9.7 us, of which 4 are start and end.
+// 5120 54.7 us, 6.5 TB/s; 32 x 16384 x 5120 9.7 us, of which 3 are start and end.
 // mx_pair_kernel (many) is paced by the tensor cores under the power cap: 4096 x
 // 16384 x 5120 with bf16 Y 125 us, 5.5 PFLOP/s.
 #include <cstring>
