@@ -146,6 +146,30 @@ def test_graphs_of_two_streams_at_once(q4):
     no_device_error(q4)
 
 
+def test_products_of_five_streams_at_once(q4):
+    """Clusters of every size and pairs of CTAs, waiting for each other's SMs."""
+    calls, want = [], []
+    for M, N, K in ((64, 1024, 5120), (128, 1024, 5120), (16, 1024, 8192), (2, 5120, 4096), (300, 2048, 1024)):
+        g = _gen(M)
+        W = torch.empty(q4.mxfp4_bytes(N, K), dtype=torch.uint8, device="cuda")
+        X = torch.empty(q4.mxfp4_bytes(M, K), dtype=torch.uint8, device="cuda")
+        Y = torch.empty((M, N), device="cuda")
+        q4.mxfp4_quantize(_randn(g, N, K), W, N, K)
+        q4.mxfp4_quantize(_randn(g, M, K), X, M, K)
+        q4.mxfp4_gemm(W, X, Y, M, N, K)
+        want.append(Y.clone())
+        Y.fill_(float("nan"))
+        calls.append((W, X, Y, M, N, K, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for c in calls:
+            q4.mxfp4_gemm(*c)
+    torch.cuda.synchronize()
+    for c, w in zip(calls, want):
+        assert torch.equal(c[2], w)
+    no_device_error(q4)
+
+
 def test_stream_arguments(q4):
     """A stream object, its handle and the current stream mean the same; the
     call waits for what is before it on that stream."""
