@@ -6,12 +6,16 @@ functions also raw device addresses), passes their pointers, sizes and the
 current CUDA stream to the C entry point of the same name, and raises
 ``Q4Error`` on a non-zero status.  All arithmetic runs in the library's CUDA kernels; there is no CPU
 path.  Importing this package fails loudly if the library has not been built
-(``python bit_weight_only_matmul_b200/build.py``), the extension module with
-its checks among it.
+(``python bit_weight_only_matmul_b200/build.py``).  The MXFP4 functions and the
+block norm need torch and the extension module with their checks
+(``_binding.so``), which the first call of one of them loads; without either
+that call fails loudly, and the Q4_0 functions work on raw addresses and
+stream handles.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 from typing import Iterable, Optional, Sequence
 
@@ -140,11 +144,22 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 lib = _lib
 
-if not os.path.exists(os.path.join(_HERE, "_binding.so")):
-    raise ImportError(f"{_HERE}/_binding.so is missing: build it with `python bit_weight_only_matmul_b200/build.py`")
-import torch  # noqa: E402, F401  (its libraries, which the extension module is linked to)
 
-from . import _binding  # noqa: E402
+class _Binding:
+    """Stands for the extension module until one of its functions is asked for;
+    importing the module then puts it into this package's ``_binding``."""
+
+    def __getattr__(self, name):
+        import torch  # noqa: F401  (its libraries, which the extension module is linked to)
+        try:
+            module = importlib.import_module("._binding", __name__)
+        except ImportError as e:
+            raise ImportError(f"{_HERE}/_binding.so does not load ({e}): build it for this torch with "
+                              "`python bit_weight_only_matmul_b200/build.py`") from e
+        return getattr(module, name)
+
+
+_binding = _Binding()
 
 
 def _ptr(t) -> Optional[int]:
