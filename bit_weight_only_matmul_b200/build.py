@@ -13,18 +13,22 @@ into _build_debug/ and libq4_0_b200_debug.so.
 
 csrc/binding.cpp, the binding's checks as a CPython extension module, is
 compiled with the host compiler against the headers of the interpreter and
-the torch it runs with, and linked to the library beside it (_binding.so).
+the torch it runs with, and linked to the library beside it (_binding.so); it
+is compiled anew when one of the two has changed, and left out, with a note,
+where there is no torch.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import subprocess
 import sys
 import sysconfig
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -87,23 +91,35 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, 
     return lib
 
 
-def build_binding(force: bool = False, verbose: bool = False) -> str:
-    """The extension module, after the library that it is linked to."""
+def build_binding(force: bool = False, verbose: bool = False) -> Optional[str]:
+    """The extension module, after the library that it is linked to; None
+    without torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = spec.submodule_search_locations[0]
     src = os.path.join(CSRC, "binding.cpp")
-    newest = max(os.path.getmtime(f) for f in (src, *glob.glob(os.path.join(INCLUDE, "*.h"))))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
-        return BINDING
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-I{sysconfig.get_paths()['include']}", "-isystem", os.path.join(torch, "include"),
-           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"), f"-I{INCLUDE}", src, "-o", tmp,
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"), f"-I{INCLUDE}", src,
            f"-L{PKG}", f"-l:{os.path.basename(LIB)}", f"-L{os.path.join(torch, 'lib')}", "-ltorch_python", "-ltorch_cpu",
            "-lc10", "-Wl,-rpath,$ORIGIN"]   # torch's own are loaded already when the module is
+    # what it was built with, beside the library's objects
+    stamp, made = os.path.join(BUILD, "binding.txt"), "\n".join([*cmd, sys.version, importlib.metadata.version("torch")])
+    newest = max(os.path.getmtime(f) for f in (src, *glob.glob(os.path.join(INCLUDE, "*.h"))))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == made:
+                return BINDING
+    cmd += ["-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(made)
     return BINDING
 
 
@@ -116,7 +132,7 @@ def main(argv=None) -> int:
     a = ap.parse_args(argv)
     print(build(a.force, a.verbose, a.ptxas_info, a.debug))
     if not a.debug:
-        print(build_binding(a.force, a.verbose))
+        print(build_binding(a.force, a.verbose) or "no torch: built without the extension module")
     return 0
 
 

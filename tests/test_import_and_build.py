@@ -1,6 +1,8 @@
 """The package without torch, or with an extension module that does not load:
 the Q4_0 functions still work with raw addresses, and the functions that need
 the extension module say why they cannot run."""
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
@@ -53,3 +55,46 @@ def test_import_without_the_extension_module():
     out = _run("bit_weight_only_matmul_b200._binding")
     assert out[:2] == ["refused 1", "refused 2"]
     assert len(out) == 5 and all(line.startswith("ImportError") and "build.py" in line for line in out[2:]), out
+
+
+def _builder(tmp_path, monkeypatch):
+    """build.py with its outputs in tmp_path and a compiler that only notes that it ran."""
+    spec = importlib.util.spec_from_file_location("q4_0_b200_build_copy", os.path.join(ROOT, "bit_weight_only_matmul_b200", "build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    ran = []
+
+    def run(cmd, **_):
+        ran.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    monkeypatch.setattr(b, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(b, "BUILD", str(tmp_path / "_build"))
+    monkeypatch.setattr(b.subprocess, "run", run)
+    return b, ran
+
+
+def test_binding_is_rebuilt_for_another_torch_or_interpreter(tmp_path, monkeypatch):
+    b, ran = _builder(tmp_path, monkeypatch)
+    b.build_binding()
+    b.build_binding()
+    assert len(ran) == 1
+    version = importlib.metadata.version
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "0.0" if name == "torch" else version(name))
+    b.build_binding()
+    b.build_binding()
+    assert len(ran) == 2
+    monkeypatch.setattr(sys, "version", "another interpreter")
+    b.build_binding()
+    b.build_binding()
+    assert len(ran) == 3
+
+
+def test_library_alone_is_built_without_torch(tmp_path, monkeypatch, capsys):
+    b, ran = _builder(tmp_path, monkeypatch)
+    monkeypatch.setattr(b, "build", lambda *a: "the library")
+    find_spec = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find_spec(name, *a))
+    assert b.main([]) == 0
+    out = capsys.readouterr().out
+    assert "the library" in out and "torch" in out and not ran
