@@ -161,16 +161,17 @@ __device__ __forceinline__ void store_columns(const SplitParams &P, uint32_t d, 
 // A warp's 32 lanes of the accumulator to the ranks that add their columns, in
 // groups of G; `mine` is the lane's row in this rank's first group.
 template <int G>
-__device__ __forceinline__ void send_columns(int live, int cpr, uint32_t d, uint32_t mine) {
+__device__ __forceinline__ void send_columns(const SplitParams &P, SplitSmem &S, int cpr, uint32_t d, uint32_t mine) {
     int dest = 0, at = 0;
     #pragma unroll 1
-    for (int c = 0; c < live; c += 8) {
+    for (int c = 0; c < P.M; c += 8) {
         float v[8];
         tc_ld_cols<8>(d + c, v);
         tc_wait_ld();
         #pragma unroll
         for (int j = 0; j < 8; j += G) {
-            if (c + j < live) {
+            if (c + j < P.M) {
+                if (Q4_DEBUG_BAD(dest < P.split && at + G <= cpr, P.err, &S.abort_flag)) return;
                 const uint32_t to = remote_addr(mine + at * 512, dest);
                 if constexpr (G == 4)
                     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v[j]), "f"(v[j + 1]),
@@ -210,7 +211,7 @@ __device__ __forceinline__ void store_sums(const SplitParams &P, const float *re
 template <int G>
 __device__ __forceinline__ void meet(const SplitParams &P, SplitSmem &S, float *red, int rank, int row, uint32_t d, int64_t n) {
     const int cpr = split_cpr(P.xcap, P.split);
-    send_columns<G>(P.M, cpr, d, smem_addr(red + rank * cpr * 128 + G * row));
+    send_columns<G>(P, S, cpr, d, smem_addr(red + rank * cpr * 128 + G * row));
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
     __syncwarp();
     const int lane = threadIdx.x & 31;
@@ -277,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
             for (; c < k1 - k0; ++c, w += kMxTileBytes) {
                 const int s = c % P.slots;
                 if (!wait_or_abort(&S.empty[s], ((c / P.slots) & 1) ^ 1, &S.abort_flag, P.err)) break;
+                if (Q4_DEBUG_BAD(s < kMaxSlots && tn < (P.N + 127) / 128 && k0 + c < P.kt, P.err, &S.abort_flag)) break;
                 mbar_arrive_expect_tx(&S.full[s], kMxTileBytes);
                 bulk_g2s(ring + s * slot_bytes, w, kMxTileBytes, &S.full[s]);
             }
@@ -290,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
             for (; c < k1 - k0; ++c, x += kMxTileBytes) {
                 const int s = c % P.slots;
                 if (!wait_or_abort(&S.empty[s], ((c / P.slots) & 1) ^ 1, &S.abort_flag, P.err)) break;
+                if (Q4_DEBUG_BAD(s < kMaxSlots && rows <= 128 && k0 + c < P.kt, P.err, &S.abort_flag)) break;
                 uint8_t *slot = ring + s * slot_bytes + kMxTileBytes;
                 mbar_arrive_expect_tx(&S.full[s], rows * 128 + 1024);
                 bulk_g2s(slot, x, rows * 128, &S.full[s]);
@@ -307,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx_split_kernel(const __grid_cons
             tc_fence_after();
             const uint32_t base = smem_addr(ring) + s * slot_bytes;
             const uint32_t sfa = sf0 + 16 * s, sfb = sfa + 8;
+            if (Q4_DEBUG_BAD(split_d_cols(P.xcap) + 16 * s + 16 <= kSplitTmemCols, P.err, &S.abort_flag)) break;
             const uint64_t a = sw128_kmajor_desc(base), b = sw128_kmajor_desc(base + kMxTileBytes);
             const uint64_t da = scales_desc(base + kMxCodeBytes), db = scales_desc(base + kMxTileBytes + x_bytes);
             __syncwarp();
@@ -567,19 +571,24 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1) mx_
 
     if (warp == 0) {
         produce<C::kSlots>(P, S, first, step, rank, kMxTileBytes, [&](const TilePlace &at, int s, int i, uint32_t bar) {
-            tma_load_pair(smem_addr(ring) + s * C::kSlotBytes, &P.map_w, 17 * (min(2 * at.n + rank, P.wt - 1) * P.kt + i), bar);
+            const int y = 17 * (min(2 * at.n + rank, P.wt - 1) * P.kt + i);
+            if (Q4_DEBUG_BAD(s < C::kSlots && y >= 0 && y + 17 <= 17 * P.wt * P.kt, P.err, &S.abort_flag)) return;
+            tma_load_pair(smem_addr(ring) + s * C::kSlotBytes, &P.map_w, y, bar);
         });
     } else if (warp == 10) {
         produce<C::kSlots>(P, S, first, step, rank, C::kXCodes, [&](const TilePlace &at, int s, int i, uint32_t bar) {
             const int y = XN == 256 ? 17 * (min(2 * at.m + rank, P.xt - 1) * P.kt + i) : 17 * (at.m * P.kt + i) + 8 * rank;
+            if (Q4_DEBUG_BAD(s < C::kSlots && y >= 0 && y + C::kXCodes / 1024 < 17 * P.xt * P.kt, P.err, &S.abort_flag)) return;
             tma_load_pair(smem_addr(ring) + s * C::kSlotBytes + kMxTileBytes, &P.map_x, y, bar);
         });
     } else if (warp == 11) {
         produce<C::kSlots>(P, S, first, step, rank, C::kXScales, [&](const TilePlace &at, int s, int i, uint32_t bar) {
             #pragma unroll
-            for (int h = 0; h < XN / 128; ++h)
-                tma_load_pair(smem_addr(ring) + s * C::kSlotBytes + kMxTileBytes + C::kXCodes + 1024 * h, &P.map_xs,
-                              17 * (min(XN / 128 * at.m + h, P.xt - 1) * P.kt + i) + 16, bar);
+            for (int h = 0; h < XN / 128; ++h) {
+                const int y = 17 * (min(XN / 128 * at.m + h, P.xt - 1) * P.kt + i) + 16;
+                if (Q4_DEBUG_BAD(s < C::kSlots && y >= 0 && y < 17 * P.xt * P.kt, P.err, &S.abort_flag)) return;
+                tma_load_pair(smem_addr(ring) + s * C::kSlotBytes + kMxTileBytes + C::kXCodes + 1024 * h, &P.map_xs, y, bar);
+            }
         });
     } else if (warp == 1 && rank == 0) {
         constexpr uint32_t idesc = mxf4_idesc(256, XN, 0);
