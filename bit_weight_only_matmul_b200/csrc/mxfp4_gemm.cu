@@ -21,7 +21,8 @@
 // mx_split_kernel (few rows) is paced by the weight stream from HBM: 1 x 131072 x
 // 5120 54.7 us, 6.5 TB/s; 32 x 16384 x 5120 9.7 us, of which 3 are start and end.
 // mx_pair_kernel (many) is paced by the tensor cores under the power cap: 4096 x
-// 16384 x 5120 with bf16 Y 125 us, 5.5 PFLOP/s.
+// 16384 x 5120 with bf16 Y 120 to 126 us (5.5 PFLOP/s) in a burst of 24, 140 to
+// 147 (4.8) in 4000 one after the other, and the same between its quantizes.
 #include <cstring>
 #include <type_traits>
 
@@ -99,7 +100,7 @@ __device__ __forceinline__ bool elect_one() {
 // sums meet in shared memory: rank q adds columns [q*cpr, (q+1)*cpr) over all
 // ranks, in rank order, so the result does not depend on timing.  They travel
 // in groups of four columns, 16 bytes a lane (128 x 1024 x 5120 8.4 us one by one,
-// 7.7 in groups), one or two columns one by one (1 x 5120 x 8192 7.2 and 7.3).
+// 7.5 in groups), one or two columns one by one (1 x 5120 x 8192 7.2 and 7.3).
 struct SplitParams {
     const uint8_t *W, *X;
     void *Y;
@@ -400,7 +401,10 @@ cudaError_t launch_split(const uint8_t *W, const uint8_t *X, void *Y, bool bf16,
     const int kt = static_cast<int>(kt64), xcap = static_cast<int>(M + 7) & ~7;
     const int64_t tiles = q4::mx_row_tiles(N);
     // K is split into the number of parts that a model of the time favours, of
-    // those that leave each CTA an SM of its own and run all at once.  The model
+    // those that leave each CTA an SM of its own; for more than 32 rows, whose
+    // CTAs take all of an SM's memory, of those whose clusters run all at once
+    // (up to 32 rows two CTAs fit an SM, and a cluster finds room beside
+    // another).  The model
     // (ns) is a fit to 150 shapes, each with every number of parts: a step of
     // a CTA costs 260 and two thirds of a row, the meeting of the sums 800 and
     // more with the rows and the CTAs; on 150 others its choice is 0.9 % slower
@@ -411,7 +415,9 @@ cudaError_t launch_split(const uint8_t *W, const uint8_t *X, void *Y, bool bf16,
     int split = 1;
     int64_t least = 0;
     for (int parts = 1; parts <= 8 && parts <= kt && (parts == 1 || tiles * parts <= dev.sm_count); ++parts) {
-        if (parts == 5 || parts == 7) continue;   // slower than their neighbours (32 x 1024 x 5120: 7 parts 5.4 us, 8 4.8)
+        // of 61 shapes 5 or 7 parts were the best for 2, by 1.1 % at most, and 7
+        // parts of more than 32 rows twice as slow where 4 or 6 still ran at once
+        if (parts == 5 || parts == 7) continue;
         if (parts > 1 && M > 32 && tiles > clusters_at_once(parts, dev)) continue;
         int64_t cost = (260 + 2 * M / 3) * ((kt + parts - 1) / parts);
         if (parts > 1) cost += 800 + 20 * M + tiles * parts * (40 + M) / 10;
@@ -724,12 +730,12 @@ cudaError_t launch_mx_gemm(const uint8_t *W, const uint8_t *X, void *Y, int y_ty
     // up to 128 rows, one tile of X, the pair kernel's weight tiles are as many
     // but go to half as many places, and it cannot split K (us, split and pair:
     // 64 x 16384 x 5120 10.2 and 10.9, 64 x 5120 x 8192 10.0 and 11.4, 64 x 1024 x 5120
-    // 5.7 and 8.3, 64 x 32768 x 5120 16.9 and 21.2, 128 x 16384 x 5120 11.1 and 11.5,
+    // 5.6 and 8.3, 64 x 32768 x 5120 16.9 and 21.2, 128 x 16384 x 5120 11.1 and 11.5,
     // 128 x 2048 x 2048 5.6 and 6.2; the other way 128 x 8192 x 5120 9.8 and 9.5)
     if (M <= q4::kMxTileRows) return launch_split(W, X, Y, bf16, M, N, kt, dev, s);
     const int64_t tiles_n = (wt + 1) / 2;
     // tiles of 128 activation rows while they all run at once, of 256 beyond
-    // (us, 128 and 256: 333 x 5003 x 4128 9.0 and 11.3, 512 x 2048 x 2048 6.2 and
+    // (us, 128 and 256: 333 x 5003 x 4128 8.9 and 11.3, 512 x 2048 x 2048 6.2 and
     // 7.9; 256 x 16384 x 5120 15.9 and 13.6, 600 x 5120 x 4096 12.6 and 11.3)
     const bool wide = tiles_n * xt > dev.sm_count / 2;
     const int64_t tiles_m = wide ? (xt + 1) / 2 : xt, tiles = tiles_n * tiles_m;

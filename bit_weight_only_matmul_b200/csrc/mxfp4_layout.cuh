@@ -12,9 +12,11 @@
 //     512 * (b / 4) + 16 * (r % 32) + 4 * (r / 32) + b % 4, the order in
 //     which a copy from shared memory lays scales into tensor memory.
 // So one contiguous copy brings a tile in the form the tensor cores take it
-// in: no tensor map, and a stream of weights reads memory front to back.
-// Blocks past K in the last tile hold zero codes and a zero scale byte; rows
-// past R are never written and never looked at.
+// in: the product of few rows needs no tensor map, and a stream of weights
+// reads memory front to back.  Blocks past K in the last tile hold zero codes
+// and a zero scale byte.  Rows past R are never written; the product copies
+// some of them or all with the tile, and the rows and columns of the
+// accumulator that they reach are never stored.
 #pragma once
 
 #include <cstdint>

@@ -4,18 +4,21 @@
 //
 // A warp takes two or eight consecutive rows of a tile (256 k, 8 values a
 // lane, four lanes a block).  It reads 512 or 1024 contiguous bytes of each
-// row, all rows before it works on the first, finds each block's largest magnitude with two
-// shuffles, and writes each row's 128 bytes of codes as one line and its
-// eight scale bytes from eight lanes.
+// row, all rows before it works on the first (pack: each row as it stores it),
+// finds each block's largest magnitude with two shuffles, and writes each
+// row's 128 bytes of codes as one line and its eight scale bytes from eight
+// lanes.
 //
-// Bound by HBM (16384 x 5120: quantize of fp32 57.8 us, 6.6 TB/s, dequant to bf16
-// 35.2 us, 6.0 TB/s), and for 16-bit values by the instructions too (quantize of
-// 8192 x 8192 bf16 29.8 us, 5.7 TB/s).  Eight rows a warp keep more in flight
-// where there are warps enough (that quantize 35.7 us against 39.9 with two
-// rows when it was chosen, dequant to bf16 35.1 against 44.2); two spread few
-// rows over the SMs (1003 x 4128 fp16 quantize 4.3 us against 5.9, now 3.7), and
-// are enough for fp32, whose rows are twice as many bytes (16384 x 5120 quantize
-// 57.8 against 59.0 us, dequant 64.0 against 72.5).
+// Quantize and dequant are bound by HBM (16384 x 5120: quantize of fp32 57.8
+// us, 6.6 TB/s, dequant to bf16 34.0 us, 6.2 TB/s), and for 16-bit values by
+// the instructions too (quantize of 8192 x 8192 bf16 29.8 us, 5.7 TB/s).  Eight
+// rows a warp keep more in flight where there are warps enough (that quantize
+// 35.7 us against 39.9 with two rows when it was chosen, dequant to bf16 35.1
+// against 44.2); two spread few rows over the SMs (1003 x 4128 fp16 quantize
+// 4.3 us against 5.9, now 3.7), and are enough for fp32, whose rows are twice as
+// many bytes (16384 x 5120 quantize 57.8 against 59.0 us, dequant 65 against
+// 72.5).  Pack, which runs once for a checkpoint, has one row's loads of a warp
+// in flight and is bound by their latency: 16384 x 5120 55 us, 1.6 TB/s.
 #include "mxfp4_layout.cuh"
 
 namespace {

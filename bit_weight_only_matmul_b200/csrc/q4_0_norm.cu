@@ -437,6 +437,11 @@ cudaError_t launch_block_norm(const q4_0_block &b, const DeviceInfo &dev, cudaSt
     if (groups <= 16) return launch_rows<1, 512, true>(b, p, groups, s);
     if (groups <= 32) return launch_rows<1, 1024, true>(b, p, groups, s);
     if (groups <= 64) return launch_rows<2, 1024, true>(b, p, (groups + 1) / 2, s);
+    // rows above 16384 values, of any number: y and r of 32768 in fp32 are more
+    // than an SM's shared memory, so there is no landing them.  With 1024 threads
+    // of 64 registers each some values spill (40 to 68 bytes a thread for two
+    // groups, 104 to 224 for four): 2000 x 20000 fp32 165 us, 3.4 TB/s, where 2000 x
+    // 16384 lands and takes 96 (4.8 TB/s); 1 x 16384 6.0 us, 1 x 32768 13.2
     return launch_rows<4, 1024, false>(b, p, (groups + 3) / 4, s);
 }
 

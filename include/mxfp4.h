@@ -16,8 +16,10 @@
  *   - from byte 16384 the scales: block b of row r at byte
  *     16384 + 512*(b/4) + 16*(r%32) + 4*(r/32) + b%4.
  * Blocks past K in the last tile hold zero codes and zero scale bytes (every
- * function here writes them so, and mxfp4_gemm relies on it); rows past R are
- * neither written nor looked at.
+ * function here writes them so, and mxfp4_gemm relies on it).  Rows past R are
+ * never written and may hold anything, no result depends on them; but
+ * mxfp4_gemm copies whole tiles and reads them too, so that all mxfp4_bytes()
+ * bytes have to be there.
  */
 #ifndef MXFP4_B200_H
 #define MXFP4_B200_H

@@ -296,7 +296,12 @@ enum {
  *                or NULL: no second norm, and pre_weight must be NULL too
  *   pre_weight   fp32 [D], or NULL
  * Arithmetic and sums are fp32; r' is rounded once to r_type, and x is taken
- * from r' before that rounding.  A row of zeros with eps == 0 gives NaN. */
+ * from r' before that rounding, a bf16 x by one more; an MXFP4 x is what
+ * mxfp4_quantize makes of the fp32 x, so that where the exact x lies next to a
+ * border of two codes its last fp32 bit decides between them.  A row of zeros
+ * with eps == 0 gives NaN.  The squares are fp32 too: a row whose squares sum to
+ * more than 3.4e38 has a norm of zeros, and with eps == 0 one whose squares are
+ * all below 7e-46 a norm of infinities. */
 typedef struct q4_0_block {
     const void *y, *r;
     void *r_out, *x;
