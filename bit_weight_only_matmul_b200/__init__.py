@@ -150,6 +150,8 @@ class _Binding:
     importing the module then puts it into this package's ``_binding``."""
 
     def __getattr__(self, name):
+        if name.startswith("__"):   # what only looks at the object
+            raise AttributeError(name)
         import torch  # noqa: F401  (its libraries, which the extension module is linked to)
         try:
             module = importlib.import_module("._binding", __name__)

@@ -98,3 +98,10 @@ def test_library_alone_is_built_without_torch(tmp_path, monkeypatch, capsys):
     assert b.main([]) == 0
     out = capsys.readouterr().out
     assert "the library" in out and "torch" in out and not ran
+
+
+def test_looking_at_the_package_needs_no_torch():
+    code = HIDE.format(hidden="torch") + "import inspect, bit_weight_only_matmul_b200 as q4\n" + \
+        "for v in vars(q4).values(): inspect.unwrap(v) if callable(v) else hasattr(v, '__wrapped__')\nprint('seen')"
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout == "seen\n", r.stderr
