@@ -42,3 +42,15 @@ def test_every_instance(q4, M, D, y):
     # of the larger of the value and what cancelled in it
     size = np.abs(wx) + 8.0 * np.abs(pre.double().cpu().numpy())
     assert np.all(np.abs(x.double().cpu().numpy() - wx) <= 2.0 ** -17 * size)
+
+
+@pytest.mark.parametrize("M", [2, 200])
+def test_squares_that_fp32_does_not_hold(q4, M):
+    """As the header says: sums of squares above 3.4e38 give a norm of zeros,
+    and with eps == 0 squares below 7e-46 = 2^-150 one of infinities."""
+    D = 512
+    big, small = torch.full((M, D), 1e18, device="cuda"), torch.full((M, D), 2.0 ** -76, device="cuda")
+    for r, eps, want in ((big, 1e-6, 0.0), (big, 0.0, 0.0), (small, 0.0, float("inf")), (0.5 * big, 1e-6, 1.0)):
+        x = torch.full((M, D), float("nan"), device="cuda")
+        q4.q4_0_block_norm(r, M, D, x=x, eps=eps)
+        assert torch.allclose(x, torch.full_like(x, want), rtol=2.0 ** -20, atol=0), (eps, want, x[0, :4])
